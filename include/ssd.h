@@ -371,6 +371,130 @@ ssd_status ssd_causal_conv1d_varlen(
     void *conv_states, int32_t num_slots, const int32_t *read_slot, const int32_t *write_slot,
     void *out, void *stream);
 
+/*
+ * Selective scan with a decay per channel and state, over the varlen layout of
+ * "[Model] Mamba2 varlen and metadata refactor" (PR #21467, Purpose). Where
+ * ssd_chunk_scan_varlen has one step size and one decay rate per head, here
+ * every channel d has a step size per token and N decay rates (group
+ * g = d / (channels/ngroups)):
+ *     delta  = softplus(dt[t,d] + dt_bias[d])
+ *     h[d,n] = exp(delta * A[d,n]) * h[d,n] + delta * u[t,d] * B[t,g,n]
+ *     y[t,d] = (sum_n h[d,n] * C[t,g,n] + D[d] * u[t,d]) * silu(z[t,d])
+ * (without the last factor when z is NULL), from initial_states[s] (if
+ * flagged; all if has_initial_state is NULL) or zero.
+ *
+ *  u, z, y         element type `in_dtype`, (T, channels); z may be NULL
+ *  dt              element type `dt_dtype`, (T, channels), raw (before bias and softplus)
+ *  B, C            element type `in_dtype`, (T, ngroups, dstate)
+ *  dt_bias, D      float32 (channels) or NULL (= 0)
+ *  A               float32 (channels, dstate)
+ *  *_stride        elements from one token's row to the next (rows themselves
+ *                  are contiguous): at least the row's length, at most 2^28.
+ *                  So halves of one projection's output are passed as they are.
+ *  initial_states, final_states  float32 (S, channels, dstate)
+ *  chunk_states    optional state export after each chunk of meta's grid, as
+ *                  for ssd_chunk_scan_varlen: chunk_states[chunk_state_dst[c]]
+ *                  (or [c] when chunk_state_dst is NULL); slots >= capacity
+ *                  raise SSD_DATA_BAD_SLOT and are skipped. The plan of
+ *                  ssd_export_chunk_states (state_elems = channels*dstate)
+ *                  feeds chunk_state_dst.
+ * Supported: any channels >= 1 (channels % ngroups == 0), dstate in
+ * {16, 32, 64, 128, 256}. y and the state outputs must not overlap an input.
+ * Precision: all arithmetic and the state in float32; y is rounded once (to
+ * nearest even). Results do not depend on the chunk size or on timing.
+ * Errors: SSD_ERR_NULL_ARG, SSD_ERR_SHAPE (sizes, strides, float32 buffers
+ * not 16-byte aligned, other buffers not aligned to their element),
+ * SSD_ERR_DTYPE, SSD_ERR_UNSUPPORTED (dstate), SSD_ERR_CHUNK_SIZE,
+ * SSD_ERR_CAPACITY, SSD_ERR_HIP. If error_flag already holds
+ * SSD_DATA_BAD_CU_SEQLENS the kernel writes nothing. Asynchronous on `stream`.
+ */
+ssd_status ssd_selective_scan_varlen(
+    const void *u, int64_t u_stride, const void *dt, int64_t dt_stride, const float *dt_bias, const float *A,
+    const void *B, int64_t B_stride, const void *C, int64_t C_stride, const float *D, const void *z,
+    int64_t z_stride, ssd_dtype in_dtype, ssd_dtype dt_dtype, const ssd_varlen_meta *meta, int32_t channels,
+    int32_t dstate, int32_t ngroups, const float *initial_states, const int32_t *has_initial_state, void *y,
+    int64_t y_stride, float *final_states, float *chunk_states, const int32_t *chunk_state_dst,
+    int32_t chunk_states_capacity, void *stream);
+
+/*
+ * The same recurrence for one new token per sequence, with the dual state
+ * anchors of ssd_decode_step: the state is read from state_cache[read_slot[s]]
+ * (zero when < 0) and written to state_cache[write_slot[s]] (skipped when < 0).
+ *  u, z, y, dt, B, C, strides  as above, with nseqs rows
+ *  state_cache     float32 (num_slots, channels, dstate), 16-byte aligned
+ *  read_slot, write_slot  int32 (nseqs). Equal slots update in place. Write
+ *                  slots must be unique and must not be another sequence's
+ *                  read slot (else unspecified).
+ *  error_flag      int32 [1] or NULL: a slot >= num_slots sets
+ *                  SSD_DATA_BAD_SLOT; that sequence is skipped entirely.
+ * Supported dstate, precision and errors as above.
+ */
+ssd_status ssd_selective_step(
+    const void *u, int64_t u_stride, const void *dt, int64_t dt_stride, const float *dt_bias, const float *A,
+    const void *B, int64_t B_stride, const void *C, int64_t C_stride, const float *D, const void *z,
+    int64_t z_stride, ssd_dtype in_dtype, ssd_dtype dt_dtype, int32_t nseqs, int32_t channels, int32_t dstate,
+    int32_t ngroups, float *state_cache, int32_t num_slots, const int32_t *read_slot, const int32_t *write_slot,
+    void *y, int64_t y_stride, int32_t *error_flag, void *stream);
+
+/*
+ * ssd_causal_conv1d_varlen for one new token per sequence (no chunk grid is
+ * needed): the window of the W-1 inputs before the token comes from
+ * conv_states[read_slot[s]] (zero when < 0), and the shifted window, which
+ * ends with the token, goes to conv_states[write_slot[s]] (skipped when < 0).
+ *  x, out          element type `in_dtype`, (nseqs, channels), rows x_stride /
+ *                  out_stride elements apart (multiples of 8, at least
+ *                  channels, at most 2^28), 16-byte aligned
+ *  weight, bias, conv_states, channels, width, activation  as for
+ *                  ssd_causal_conv1d_varlen
+ *  read_slot, write_slot  int32 (nseqs) or NULL (= all -1). Equal slots update
+ *                  in place; otherwise write slots must be unique and must not
+ *                  be another sequence's read slot.
+ *  error_flag      int32 [1] or NULL: a slot >= num_slots sets
+ *                  SSD_DATA_BAD_SLOT; that sequence is skipped entirely.
+ * Arithmetic and rounding are those of ssd_causal_conv1d_varlen.
+ * Errors: SSD_ERR_DTYPE, SSD_ERR_SHAPE, SSD_ERR_UNSUPPORTED, SSD_ERR_NULL_ARG,
+ * SSD_ERR_HIP.
+ */
+ssd_status ssd_causal_conv1d_step(
+    const void *x, int64_t x_stride, const float *weight, const float *bias, ssd_dtype in_dtype, int32_t nseqs,
+    int32_t channels, int32_t width, int32_t activation, void *conv_states, int32_t num_slots,
+    const int32_t *read_slot, const int32_t *write_slot, void *out, int64_t out_stride, int32_t *error_flag,
+    void *stream);
+
+/* What ssd_group_norm does beside the norm. */
+typedef enum {
+    SSD_NORM_NONE = 0,        /* out = norm(x) */
+    SSD_NORM_SILU = 1,        /* out = silu(norm(x)) */
+    SSD_NORM_GATE_FIRST = 2,  /* out = norm(x * silu(z)) */
+    SSD_NORM_GATE_LAST = 3    /* out = norm(x) * silu(z) */
+} ssd_norm_act;
+
+/*
+ * Norm of groups of channels with an activation, channels last: what stands
+ * between a scan (or the gated delta rule) and the output projection. Every
+ * token is normed by itself; its channels fall into ngroups groups of
+ * k = channels/ngroups. Per token and group, with v = x (or x * silu(z)):
+ *     mu  = center ? mean(v) : 0
+ *     out = (v - mu) / sqrt(mean((v - mu)^2) + eps) * weight[c] + bias[c]
+ * then the activation. Scan outputs (T, H, P) are rows of H*P channels.
+ *  x, z, out       element type `in_dtype`, (rows, channels), rows *_stride
+ *                  elements apart (at least channels, at most 2^28); z is read
+ *                  only by the gated forms. out may be x itself.
+ *  weight, bias    float32 (channels) or NULL (= 1, 0)
+ * Supported: any channels % ngroups == 0 with groups of at most 16384
+ * channels; eps >= 0.
+ * Precision: float32; the variance is the mean of squared differences from
+ * the mean (two passes over values held on chip); one rounding to nearest
+ * even at the end.
+ * Errors: SSD_ERR_DTYPE, SSD_ERR_SHAPE (sizes, strides, alignment to the
+ * element, eps), SSD_ERR_UNSUPPORTED (activation, group size),
+ * SSD_ERR_NULL_ARG, SSD_ERR_HIP.
+ */
+ssd_status ssd_group_norm(
+    const void *x, int64_t x_stride, const void *z, int64_t z_stride, const float *weight, const float *bias,
+    ssd_dtype in_dtype, int32_t rows, int32_t channels, int32_t ngroups, float eps, int32_t center,
+    ssd_norm_act act, void *out, int64_t out_stride, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -23,6 +23,42 @@ ssd_status check_meta(const ssd_varlen_meta *m) {
     return SSD_OK;
 }
 
+bool aligned_to(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+bool known_dtype(ssd_dtype t) { return t == SSD_F32 || t == SSD_BF16; }
+
+uintptr_t elem_bytes(ssd_dtype t) { return t == SSD_BF16 ? 2 : 4; }
+
+// Rows of `row` contiguous elements, `stride` elements apart. The bound keeps
+// every byte offset inside a few rows below 2^32.
+bool row_stride(int64_t stride, int64_t row) { return stride >= row && stride <= (int64_t(1) << 28); }
+
+// What the selective scan and its step ask of their shared arguments.
+ssd_status check_selective(const ssd::SelectiveArgs &a, ssd_dtype in_dtype, ssd_dtype dt_dtype, bool rows) {
+    if (!known_dtype(in_dtype) || !known_dtype(dt_dtype)) return SSD_ERR_DTYPE;
+    if (a.C_total <= 0 || a.N <= 0 || a.G <= 0 || a.C_total % a.G != 0) return SSD_ERR_SHAPE;
+    if (!(a.N == 16 || a.N == 32 || a.N == 64 || a.N == 128 || a.N == 256)) return SSD_ERR_UNSUPPORTED;
+    if (a.A == nullptr) return SSD_ERR_NULL_ARG;
+    if (rows && (a.u == nullptr || a.dt == nullptr || a.B == nullptr || a.C == nullptr || a.y == nullptr))
+        return SSD_ERR_NULL_ARG;
+    const int64_t C = a.C_total, GN = (int64_t)a.G * a.N;
+    if (GN > (int64_t(1) << 28)) return SSD_ERR_SHAPE;
+    if (rows && (!row_stride(a.u_stride, C) || !row_stride(a.dt_stride, C) || !row_stride(a.y_stride, C) ||
+                 !row_stride(a.B_stride, GN) || !row_stride(a.C_stride, GN) ||
+                 (a.z != nullptr && !row_stride(a.z_stride, C))))
+        return SSD_ERR_SHAPE;
+    const uintptr_t e = elem_bytes(in_dtype);
+    for (const void *p : {a.u, a.B, a.C, a.z, (const void *)a.y})
+        if (!aligned_to(p, e)) return SSD_ERR_SHAPE;
+    if (!aligned_to(a.dt, elem_bytes(dt_dtype))) return SSD_ERR_SHAPE;
+    for (const void *p : {(const void *)a.A, (const void *)a.init, (const void *)a.final_states,
+                          (const void *)a.chunk_states, (const void *)a.cache})
+        if (!aligned16(p)) return SSD_ERR_SHAPE;
+    for (const void *p : {(const void *)a.dt_bias, (const void *)a.D})
+        if (!aligned_to(p, 4)) return SSD_ERR_SHAPE;
+    return SSD_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -286,6 +322,120 @@ ssd_status ssd_prefill_bites(int32_t nseqs, const int32_t *num_computed_tokens, 
         num_scheduled[s] = (int32_t)(stop - pos);
     }
     return SSD_OK;
+}
+
+ssd_status ssd_selective_scan_varlen(const void *u, int64_t u_stride, const void *dt, int64_t dt_stride,
+                                     const float *dt_bias, const float *A, const void *B, int64_t B_stride,
+                                     const void *C, int64_t C_stride, const float *D, const void *z,
+                                     int64_t z_stride, ssd_dtype in_dtype, ssd_dtype dt_dtype,
+                                     const ssd_varlen_meta *meta, int32_t channels, int32_t dstate, int32_t ngroups,
+                                     const float *initial_states, const int32_t *has_initial_state, void *y,
+                                     int64_t y_stride, float *final_states, float *chunk_states,
+                                     const int32_t *chunk_state_dst, int32_t chunk_states_capacity, void *stream) {
+    ssd_status st = check_meta(meta);
+    if (st != SSD_OK) return st;
+    ssd::SelectiveArgs a{};
+    a.u = u; a.dt = dt; a.B = B; a.C = C; a.z = z; a.dt_bias = dt_bias; a.A = A; a.D = D; a.y = y;
+    a.u_stride = u_stride; a.dt_stride = dt_stride; a.B_stride = B_stride; a.C_stride = C_stride;
+    a.z_stride = z_stride; a.y_stride = y_stride;
+    a.S = meta->nseqs; a.T = meta->total_tokens; a.C_total = channels; a.N = dstate; a.G = ngroups;
+    a.error_flag = meta->error_flag;
+    a.init = initial_states; a.has_init = has_initial_state; a.final_states = final_states;
+    a.chunk_states = chunk_states; a.chunk_state_dst = chunk_state_dst;
+    a.cu_seqlens = meta->cu_seqlens; a.seq_chunk_start = meta->seq_chunk_start; a.seq_order = meta->seq_order;
+    a.cs = meta->chunk_size; a.max_chunks = meta->max_chunks;
+    a.capacity = chunk_states != nullptr ? chunk_states_capacity : 0;
+    st = check_selective(a, in_dtype, dt_dtype, meta->total_tokens > 0);
+    if (st != SSD_OK) return st;
+    if (meta->nseqs > 0 && final_states == nullptr) return SSD_ERR_NULL_ARG;
+    if (chunk_states != nullptr) {
+        if (chunk_states_capacity <= 0) return SSD_ERR_CAPACITY;
+        if (chunk_state_dst == nullptr && chunk_states_capacity < meta->max_chunks) return SSD_ERR_CAPACITY;
+    }
+    if (meta->nseqs == 0) return SSD_OK;
+    return ssd::launch_selective_scan(a, in_dtype == SSD_BF16, dt_dtype == SSD_BF16,
+                                      static_cast<hipStream_t>(stream)) == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+
+ssd_status ssd_selective_step(const void *u, int64_t u_stride, const void *dt, int64_t dt_stride,
+                              const float *dt_bias, const float *A, const void *B, int64_t B_stride, const void *C,
+                              int64_t C_stride, const float *D, const void *z, int64_t z_stride, ssd_dtype in_dtype,
+                              ssd_dtype dt_dtype, int32_t nseqs, int32_t channels, int32_t dstate, int32_t ngroups,
+                              float *state_cache, int32_t num_slots, const int32_t *read_slot,
+                              const int32_t *write_slot, void *y, int64_t y_stride, int32_t *error_flag,
+                              void *stream) {
+    if (nseqs < 0 || num_slots < 0) return SSD_ERR_SHAPE;
+    ssd::SelectiveArgs a{};
+    a.u = u; a.dt = dt; a.B = B; a.C = C; a.z = z; a.dt_bias = dt_bias; a.A = A; a.D = D; a.y = y;
+    a.u_stride = u_stride; a.dt_stride = dt_stride; a.B_stride = B_stride; a.C_stride = C_stride;
+    a.z_stride = z_stride; a.y_stride = y_stride;
+    a.S = nseqs; a.T = nseqs; a.C_total = channels; a.N = dstate; a.G = ngroups;
+    a.error_flag = error_flag;
+    a.cache = state_cache; a.num_slots = num_slots; a.read_slot = read_slot; a.write_slot = write_slot;
+    const ssd_status st = check_selective(a, in_dtype, dt_dtype, nseqs > 0);
+    if (st != SSD_OK) return st;
+    if (nseqs == 0) return SSD_OK;
+    if (state_cache == nullptr || read_slot == nullptr || write_slot == nullptr) return SSD_ERR_NULL_ARG;
+    return ssd::launch_selective_step(a, in_dtype == SSD_BF16, dt_dtype == SSD_BF16,
+                                      static_cast<hipStream_t>(stream)) == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+
+ssd_status ssd_causal_conv1d_step(const void *x, int64_t x_stride, const float *weight, const float *bias,
+                                  ssd_dtype in_dtype, int32_t nseqs, int32_t channels, int32_t width,
+                                  int32_t activation, void *conv_states, int32_t num_slots,
+                                  const int32_t *read_slot, const int32_t *write_slot, void *out,
+                                  int64_t out_stride, int32_t *error_flag, void *stream) {
+    if (!known_dtype(in_dtype)) return SSD_ERR_DTYPE;
+    if (nseqs < 0 || channels <= 0 || num_slots < 0) return SSD_ERR_SHAPE;
+    if (channels % 8 != 0 || width < 1 || width > 4 || (activation != 0 && activation != 1))
+        return SSD_ERR_UNSUPPORTED;
+    if (weight == nullptr || (nseqs > 0 && (x == nullptr || out == nullptr))) return SSD_ERR_NULL_ARG;
+    if (width > 1 && num_slots > 0 && (read_slot != nullptr || write_slot != nullptr) && conv_states == nullptr)
+        return SSD_ERR_NULL_ARG;
+    if (nseqs > 0 && (!row_stride(x_stride, channels) || !row_stride(out_stride, channels) || x_stride % 8 != 0 ||
+                      out_stride % 8 != 0))
+        return SSD_ERR_SHAPE;
+    for (const void *p : {x, (const void *)out, (const void *)conv_states})
+        if (!aligned16(p)) return SSD_ERR_SHAPE;
+    for (const void *p : {(const void *)weight, (const void *)bias})
+        if (!aligned_to(p, 4)) return SSD_ERR_SHAPE;
+    if (nseqs == 0) return SSD_OK;
+    ssd::Conv1dStepArgs a{};
+    a.x = x; a.weight = weight; a.bias = bias; a.out = out; a.states = conv_states;
+    a.read_slot = read_slot; a.write_slot = write_slot; a.error_flag = error_flag;
+    a.x_stride = x_stride; a.out_stride = out_stride;
+    a.S = nseqs; a.C = channels; a.W = width; a.silu = activation;
+    a.num_slots = (conv_states != nullptr || width == 1) ? num_slots : 0;   // (width 1 keeps no rows)
+    return ssd::launch_conv1d_step(a, in_dtype == SSD_BF16, static_cast<hipStream_t>(stream)) == hipSuccess
+               ? SSD_OK : SSD_ERR_HIP;
+}
+
+ssd_status ssd_group_norm(const void *x, int64_t x_stride, const void *z, int64_t z_stride, const float *weight,
+                          const float *bias, ssd_dtype in_dtype, int32_t rows, int32_t channels, int32_t ngroups,
+                          float eps, int32_t center, ssd_norm_act act, void *out, int64_t out_stride,
+                          void *stream) {
+    if (!known_dtype(in_dtype)) return SSD_ERR_DTYPE;
+    if (rows < 0 || channels <= 0 || ngroups <= 0 || channels % ngroups != 0 || !(eps >= 0.0f))
+        return SSD_ERR_SHAPE;
+    if (act < SSD_NORM_NONE || act > SSD_NORM_GATE_LAST || channels / ngroups > ssd::kNormMaxGroup)
+        return SSD_ERR_UNSUPPORTED;
+    const bool gated = act == SSD_NORM_GATE_FIRST || act == SSD_NORM_GATE_LAST;
+    if (rows > 0 && (x == nullptr || out == nullptr || (gated && z == nullptr))) return SSD_ERR_NULL_ARG;
+    if (rows > 0 && (!row_stride(x_stride, channels) || !row_stride(out_stride, channels) ||
+                     (gated && !row_stride(z_stride, channels))))
+        return SSD_ERR_SHAPE;
+    for (const void *p : {x, gated ? z : nullptr, (const void *)out})
+        if (!aligned_to(p, elem_bytes(in_dtype))) return SSD_ERR_SHAPE;
+    for (const void *p : {(const void *)weight, (const void *)bias})
+        if (!aligned_to(p, 4)) return SSD_ERR_SHAPE;
+    if (rows == 0) return SSD_OK;
+    ssd::NormArgs a{};
+    a.x = x; a.z = gated ? z : nullptr; a.weight = weight; a.bias = bias; a.out = out;
+    a.x_stride = x_stride; a.z_stride = z_stride; a.out_stride = out_stride;
+    a.rows = rows; a.groups = ngroups; a.size = channels / ngroups;
+    a.eps = eps; a.center = center != 0; a.act = act;
+    return ssd::launch_group_norm(a, in_dtype == SSD_BF16, static_cast<hipStream_t>(stream)) == hipSuccess
+               ? SSD_OK : SSD_ERR_HIP;
 }
 
 }  // extern "C"

@@ -234,4 +234,66 @@ hipError_t launch_conv1d(const Conv1dArgs &a, bool bf16, hipStream_t stream) {
     return bf16 ? launch_conv1d_t<__bf16>(a, stream) : launch_conv1d_t<float>(a, stream);
 }
 
+// One new token per sequence: the same convolution, its window read from one
+// slot and written, shifted by the token, to another. Memory-bound and small:
+// each lane owns 8 channels of one sequence.
+template <typename T, int W>
+__global__ __launch_bounds__(kConvThreads) void ssd_conv1d_step_kernel(Conv1dStepArgs a) {
+    constexpr int WR = W > 1 ? W - 1 : 1;   // window rows (at least one, unused when W = 1)
+    using IO = ConvIO<T>;
+    const int per = kConvThreads * kConvVec, nxb = (a.C + per - 1) / per;
+    const int s = blockIdx.x / nxb;
+    const int ch = ((blockIdx.x - s * nxb) * kConvThreads + threadIdx.x) * kConvVec;
+    if (ch >= a.C) return;
+    const int rs = a.read_slot != nullptr ? a.read_slot[s] : -1;
+    const int ws = a.write_slot != nullptr ? a.write_slot[s] : -1;
+    if (rs >= a.num_slots || ws >= a.num_slots) {   // refused: nothing read or written
+        if (ch == 0 && a.error_flag != nullptr) atomicOr(a.error_flag, SSD_DATA_BAD_SLOT);
+        return;
+    }
+    const int64_t C = a.C, slot_elems = (int64_t)(W - 1) * C;
+    float win[WR][kConvVec], xv[kConvVec], o[kConvVec];
+    IO::load(a.x, (int64_t)s * a.x_stride + ch, xv);
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) {
+        if (rs >= 0) IO::load(a.states, rs * slot_elems + i * C + ch, win[i]);
+        else {
+#pragma unroll
+            for (int v = 0; v < kConvVec; ++v) win[i][v] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < kConvVec; ++v) {
+        const float *w = a.weight + (int64_t)(ch + v) * W;
+        float z = a.bias != nullptr ? a.bias[ch + v] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) z = fmaf(w[k], win[k][v], z);
+        z = fmaf(w[W - 1], xv[v], z);
+        o[v] = a.silu ? silu(z) : z;
+    }
+    IO::store(a.out, (int64_t)s * a.out_stride + ch, o, false);
+    if (ws >= 0) {
+#pragma unroll
+        for (int i = 0; i + 1 < W - 1; ++i) IO::store(a.states, ws * slot_elems + i * C + ch, win[i + 1], false);
+        if constexpr (W > 1) IO::store(a.states, ws * slot_elems + (W - 2) * C + ch, xv, false);
+    }
+}
+
+template <typename T>
+static hipError_t launch_conv1d_step_t(const Conv1dStepArgs &a, hipStream_t stream) {
+    const dim3 grid((unsigned)((int64_t)a.S * conv1d_channel_blocks(a.C))), block(kConvThreads);
+    switch (a.W) {
+        case 1: hipLaunchKernelGGL((ssd_conv1d_step_kernel<T, 1>), grid, block, 0, stream, a); break;
+        case 2: hipLaunchKernelGGL((ssd_conv1d_step_kernel<T, 2>), grid, block, 0, stream, a); break;
+        case 3: hipLaunchKernelGGL((ssd_conv1d_step_kernel<T, 3>), grid, block, 0, stream, a); break;
+        case 4: hipLaunchKernelGGL((ssd_conv1d_step_kernel<T, 4>), grid, block, 0, stream, a); break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_conv1d_step(const Conv1dStepArgs &a, bool bf16, hipStream_t stream) {
+    return bf16 ? launch_conv1d_step_t<__bf16>(a, stream) : launch_conv1d_step_t<float>(a, stream);
+}
+
 }  // namespace ssd

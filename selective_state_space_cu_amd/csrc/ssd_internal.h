@@ -136,6 +136,55 @@ constexpr size_t kGdnScratchBytes = size_t(32) << 20;
 constexpr int kMaxDevices = 64;
 hipError_t gdn_scratch(void **ptr);
 
+// Selective scan with a decay per channel and state (see ssd_selective.hip):
+// prompts (tokens of packed sequences) and single tokens (one row each).
+struct SelectiveArgs {
+    const void *u, *dt, *B, *C, *z;     // z null: no gate
+    const float *dt_bias, *A, *D;       // dt_bias, D null: 0
+    void *y;
+    int64_t u_stride, dt_stride, B_stride, C_stride, z_stride, y_stride;   // elements between rows
+    int32_t S, T, C_total, N, G;        // sequences, tokens, channels, dstate, groups
+    int32_t *error_flag;
+    // prompts
+    const float *init;                  // (S, channels, N) or null
+    const int32_t *has_init;            // (S) or null
+    float *final_states, *chunk_states;
+    const int32_t *chunk_state_dst;     // slot per chunk or null (-> chunk index)
+    const int32_t *cu_seqlens, *seq_chunk_start, *seq_order;
+    int32_t cs, capacity, max_chunks;
+    // single tokens
+    float *cache;                       // (num_slots, channels, N)
+    const int32_t *read_slot, *write_slot;
+    int32_t num_slots;
+};
+hipError_t launch_selective_scan(const SelectiveArgs &a, bool bf16, bool dt_bf16, hipStream_t stream);
+hipError_t launch_selective_step(const SelectiveArgs &a, bool bf16, bool dt_bf16, hipStream_t stream);
+
+// Causal conv1d of one token per sequence (see ssd_conv1d.hip).
+struct Conv1dStepArgs {
+    const void *x;
+    const float *weight, *bias;         // bias null: 0
+    void *out, *states;
+    const int32_t *read_slot, *write_slot;   // null: all -1
+    int32_t *error_flag;                // nullable
+    int64_t x_stride, out_stride;
+    int32_t S, C, W, num_slots, silu;
+};
+hipError_t launch_conv1d_step(const Conv1dStepArgs &a, bool bf16, hipStream_t stream);
+
+// Norm of groups of channels with an activation (see ssd_norm.hip).
+struct NormArgs {
+    const void *x, *z;
+    const float *weight, *bias;         // nullable
+    void *out;
+    int64_t x_stride, z_stride, out_stride;
+    int32_t rows, groups, size;         // size: channels of a group
+    float eps;
+    int32_t center, act;
+};
+constexpr int32_t kNormMaxGroup = 16384;
+hipError_t launch_group_norm(const NormArgs &a, bool bf16, hipStream_t stream);
+
 struct MetaArgs {
     const int32_t *cu_seqlens;
     int32_t *chunk_offsets, *chunk_seq_idx, *seq_chunk_start, *nchunks, *seq_order, *error_flag;

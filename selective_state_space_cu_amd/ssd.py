@@ -17,6 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libssd.so")
 
 SSD_F32, SSD_BF16 = 0, 1
+NORM_ACTS = {"none": 0, "silu": 1, "gate_first": 2, "gate_last": 3}   # ssd_norm_act
 DATA_BAD_CU_SEQLENS, DATA_TOO_MANY_CHUNKS, DATA_BAD_SLOT, DATA_BAD_BLOCK = 1, 2, 4, 8
 
 # names exported by libssd.so (checked by the CPU tests against include/ssd.h)
@@ -24,6 +25,7 @@ EXPORTS = ("ssd_varlen_metadata", "ssd_chunk_scan_varlen", "ssd_export_chunk_sta
            "ssd_decode_step", "ssd_causal_conv1d_varlen", "ssd_gated_delta_chunk_varlen", "ssd_gated_delta_workspace_size",
            "ssd_gated_delta_chunk_varlen_noalloc",
            "ssd_prefill_bites",
+           "ssd_selective_scan_varlen", "ssd_selective_step", "ssd_causal_conv1d_step", "ssd_group_norm",
            "ssd_status_string")
 
 
@@ -83,6 +85,18 @@ def load_library(path: str = LIB_PATH):
                                                          vp, vp, i32, vp]
     lib.ssd_gated_delta_workspace_size.restype = ctypes.c_size_t
     lib.ssd_gated_delta_workspace_size.argtypes = [i32, i32]
+    i64 = ctypes.c_int64
+    lib.ssd_selective_scan_varlen.restype = st
+    lib.ssd_selective_scan_varlen.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp, i64, st, st,
+                                              ctypes.POINTER(_Meta), i32, i32, i32, vp, vp, vp, i64, vp, vp, vp,
+                                              i32, vp]
+    lib.ssd_selective_step.restype = st
+    lib.ssd_selective_step.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp, i64, st, st, i32, i32,
+                                       i32, i32, vp, i32, vp, vp, vp, i64, vp, vp]
+    lib.ssd_causal_conv1d_step.restype = st
+    lib.ssd_causal_conv1d_step.argtypes = [vp, i64, vp, vp, st, i32, i32, i32, i32, vp, i32, vp, vp, vp, i64, vp, vp]
+    lib.ssd_group_norm.restype = st
+    lib.ssd_group_norm.argtypes = [vp, i64, vp, i64, vp, vp, st, i32, i32, i32, ctypes.c_float, i32, st, vp, i64, vp]
     lib.ssd_prefill_bites.restype = st
     lib.ssd_prefill_bites.argtypes = [i32, vp, vp, vp, i32, vp]
     _lib = lib
@@ -450,4 +464,189 @@ def causal_conv1d_varlen(x: torch.Tensor, weight: torch.Tensor, meta: VarlenMeta
         _ptr(x), _ptr(weight), _ptr(bias), _dtype_code(x), ctypes.byref(m), C, W, int(bool(silu)),
         _ptr(conv_states), 0 if conv_states is None else conv_states.shape[0], _ptr(rs), _ptr(ws),
         _ptr(out), _stream(device)))
+    return out
+
+
+def _enqueue(fn, device, *args):
+    """Call the library's `fn` on the current stream of `device`, with that device current."""
+    if device.type != "cuda":
+        raise ValueError(f"{fn} needs tensors on a GPU, got {device}")
+    f = getattr(load_library(), fn)
+    if device.index == torch.cuda.current_device():
+        status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    if status != 0:
+        raise SSDError(fn, status, status_string(status))
+
+
+def _address(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, device, dtype, shape) -> int:
+    """A tensor of `shape` (rows first) whose rows are contiguous but may lie any distance apart, as a slice of
+    a wider projection has them. Returns the elements from one row to the next."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    row = 1
+    for size, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != row:
+            raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
+        row *= size
+    return t.stride(0) if shape[0] > 1 else row
+
+
+def _params(device, **named):
+    """float32 parameters and states: (tensor or None, shape) by name."""
+    for name, (t, shape) in named.items():
+        if t is not None:
+            _shape(t, name, *shape)
+            _data(t, name, device, torch.float32)
+
+
+def _out_rows(out: Optional[torch.Tensor], name: str, like: torch.Tensor):
+    """The output and the elements between its rows: `out` if given, else a new contiguous one."""
+    if out is None:
+        out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    return out, _rows(out, name, like.device, like.dtype, like.shape)
+
+
+def _selective_inputs(u, dt, A, B, C, dt_bias, D, z):
+    """Checks what the selective scan and its step share; returns the library's leading arguments and sizes."""
+    if u.dim() != 2 or B.dim() != 3:
+        raise ValueError(f"u must be (rows, channels) and B (rows, groups, states), got {tuple(u.shape)} and "
+                         f"{tuple(B.shape)}")
+    device, dtype = u.device, u.dtype
+    if dt.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"dt must be float32 or bfloat16, got {dt.dtype}")
+    rows, channels = u.shape
+    groups, n = B.shape[1], B.shape[2]
+    strides = [_rows(u, "u", device, dtype, u.shape), _rows(dt, "dt", device, dt.dtype, u.shape),
+               _rows(B, "B", device, dtype, B.shape), _rows(C, "C", device, dtype, B.shape),
+               0 if z is None else _rows(z, "z", device, dtype, u.shape)]
+    if B.shape[0] != rows:
+        raise ValueError(f"B must have {rows} rows, got {B.shape[0]}")
+    _params(device, A=(A, (channels, n)), dt_bias=(dt_bias, (channels,)), D=(D, (channels,)))
+    return (u.data_ptr(), strides[0], dt.data_ptr(), strides[1], _address(dt_bias), A.data_ptr(), B.data_ptr(),
+            strides[2], C.data_ptr(), strides[3], _address(D), _address(z), strides[4], _dtype_code(u),
+            _dtype_code(dt)), channels, n, groups
+
+
+def selective_scan_varlen(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                          meta: VarlenMeta, dt_bias: Optional[torch.Tensor] = None,
+                          D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                          initial_states: Optional[torch.Tensor] = None,
+                          has_initial_state: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                          final_states: Optional[torch.Tensor] = None, chunk_states: Optional[torch.Tensor] = None,
+                          chunk_state_dst: Optional[torch.Tensor] = None):
+    """ssd_selective_scan_varlen: the scan with a decay per channel and state. u, dt, z (T, D) and B, C (T, G, N)
+    may be slices with rows further apart; A (D, N), dt_bias, D (D,) and the states (S, D, N) are float32.
+    `chunk_states` (float32 [slots, D, N]) receives the state after each chunk, at index c or at
+    chunk_state_dst[c] when given. Returns (y, final_states)."""
+    head, channels, n, groups = _selective_inputs(u, dt, A, B, C, dt_bias, D, z)
+    device = u.device
+    if u.shape[0] != meta.total_tokens:
+        raise ValueError(f"u has {u.shape[0]} tokens, the metadata {meta.total_tokens}")
+    states = (meta.nseqs, channels, n)
+    cap = 0 if chunk_states is None else chunk_states.shape[0]
+    _params(device, initial_states=(initial_states, states), final_states=(final_states, states),
+            chunk_states=(chunk_states, (cap, channels, n)))
+    if has_initial_state is not None:
+        _shape(has_initial_state, "has_initial_state", meta.nseqs)
+        has_initial_state = _index(has_initial_state, device)
+    _dst_len(chunk_state_dst, meta)
+    if chunk_state_dst is not None:
+        chunk_state_dst = _index(chunk_state_dst, device)
+    y, y_stride = _out_rows(y, "y", u)
+    if final_states is None:
+        final_states = torch.empty(states, dtype=torch.float32, device=device)
+    m = meta.c_struct()
+    _enqueue("ssd_selective_scan_varlen", device, *head, ctypes.byref(m), channels, n, groups,
+             _address(initial_states), _address(has_initial_state), y.data_ptr(), y_stride, final_states.data_ptr(),
+             _address(chunk_states), _address(chunk_state_dst), cap)
+    return y, final_states
+
+
+def selective_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                   state_cache: torch.Tensor, read_slot: torch.Tensor, write_slot: torch.Tensor,
+                   dt_bias: Optional[torch.Tensor] = None, D: Optional[torch.Tensor] = None,
+                   z: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                   error_flag: Optional[torch.Tensor] = None):
+    """ssd_selective_step: one token per sequence, the state read from state_cache[read_slot[s]] (zero if < 0) and
+    written to state_cache[write_slot[s]] (skipped if < 0). u, dt, z (S, D), B, C (S, G, N), state_cache float32
+    (slots, D, N). Returns y (S, D)."""
+    head, channels, n, groups = _selective_inputs(u, dt, A, B, C, dt_bias, D, z)
+    device, nseqs = u.device, u.shape[0]
+    _params(device, state_cache=(state_cache, (state_cache.shape[0], channels, n)))
+    _shape(read_slot, "read_slot", nseqs)
+    _shape(write_slot, "write_slot", nseqs)
+    rs, ws = _index(read_slot, device), _index(write_slot, device)
+    if error_flag is not None:
+        _data(error_flag, "error_flag", device, torch.int32)
+    y, y_stride = _out_rows(y, "y", u)
+    _enqueue("ssd_selective_step", device, *head, nseqs, channels, n, groups, state_cache.data_ptr(),
+             state_cache.shape[0], rs.data_ptr(), ws.data_ptr(), y.data_ptr(), y_stride, _address(error_flag))
+    return y
+
+
+def causal_conv1d_step(x: torch.Tensor, weight: torch.Tensor, conv_states: Optional[torch.Tensor] = None,
+                       read_slot: Optional[torch.Tensor] = None, write_slot: Optional[torch.Tensor] = None,
+                       bias: Optional[torch.Tensor] = None, silu: bool = True, out: Optional[torch.Tensor] = None,
+                       error_flag: Optional[torch.Tensor] = None):
+    """ssd_causal_conv1d_step: causal_conv1d_varlen for one token per sequence. x (S, C) may be a slice with rows
+    further apart; the window of W-1 inputs comes from conv_states[read_slot[s]] (zero if < 0) and goes, shifted by
+    x, to conv_states[write_slot[s]] (skipped if < 0). Returns out (S, C)."""
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError(f"x must be (sequences, channels) and weight (channels, width), got {tuple(x.shape)} and "
+                         f"{tuple(weight.shape)}")
+    device = x.device
+    nseqs, channels = x.shape
+    width = weight.shape[1]
+    x_stride = _rows(x, "x", device, x.dtype, x.shape)
+    _params(device, weight=(weight, (channels, width)), bias=(bias, (channels,)))
+    if conv_states is not None:
+        _shape(conv_states, "conv_states", conv_states.shape[0], width - 1, channels)
+        _data(conv_states, "conv_states", device, x.dtype)
+    for name, t in (("read_slot", read_slot), ("write_slot", write_slot)):
+        _shape(t, name, nseqs)
+    rs = None if read_slot is None else _index(read_slot, device)
+    ws = None if write_slot is None else _index(write_slot, device)
+    if error_flag is not None:
+        _data(error_flag, "error_flag", device, torch.int32)
+    out, out_stride = _out_rows(out, "out", x)
+    _enqueue("ssd_causal_conv1d_step", device, x.data_ptr(), x_stride, weight.data_ptr(), _address(bias),
+             _dtype_code(x), nseqs, channels, width, int(bool(silu)), _address(conv_states),
+             0 if conv_states is None else conv_states.shape[0], _address(rs), _address(ws), out.data_ptr(),
+             out_stride, _address(error_flag))
+    return out
+
+
+def group_norm(x: torch.Tensor, ngroups: int, weight: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None, act: str = "none",
+               center: bool = True, eps: float = 1e-5, out: Optional[torch.Tensor] = None):
+    """ssd_group_norm: every row of x (rows, C), or of a scan's output (T, H, P) read as T rows of H*P channels, is
+    normed in `ngroups` groups of channels (mean and variance, or the mean square alone when `center` is false),
+    scaled by weight and bias (C,), with act "none", "silu" (of the result), "gate_first" (norm of x silu(z)) or
+    "gate_last" (norm of x, times silu(z)). Rows of x and z may lie further apart. Returns out, shaped like x."""
+    if x.dim() < 2:
+        raise ValueError(f"x must have rows and channels, got {tuple(x.shape)}")
+    if act not in NORM_ACTS:
+        raise ValueError(f"act must be one of {sorted(NORM_ACTS)}, got {act!r}")
+    if (z is not None) != act.startswith("gate"):
+        raise ValueError("z is given exactly with the gated forms")
+    device = x.device
+    channels = x.shape[1:].numel()
+    x_stride = _rows(x, "x", device, x.dtype, x.shape)
+    z_stride = 0 if z is None else _rows(z, "z", device, x.dtype, x.shape)
+    _params(device, weight=(weight, (channels,)), bias=(bias, (channels,)))
+    out, out_stride = _out_rows(out, "out", x)
+    _enqueue("ssd_group_norm", device, x.data_ptr(), x_stride, _address(z), z_stride, _address(weight),
+             _address(bias), _dtype_code(x), x.shape[0], channels, int(ngroups), float(eps), int(bool(center)),
+             NORM_ACTS[act], out.data_ptr(), out_stride)
     return out
