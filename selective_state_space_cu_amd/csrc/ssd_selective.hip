@@ -10,8 +10,13 @@
 // Lanes: a wave owns 16 channels; lane = 16 q + c holds the states
 // n = q N/4 .. (q + 1) N/4 - 1 of channel c.
 #include "ssd_scan.hpp"
+#ifndef SEL_SEG
+#define SEL_SEG 8
+#endif
 
 namespace ssd {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // log(1 + e^v) in float32. For small e^v the logarithm's own argument 1 + e^v
 // has lost the digits that count, so its series is summed instead
@@ -36,65 +41,290 @@ template <typename T> __device__ __forceinline__ float load_f(const void *p, int
     return (float)reinterpret_cast<const T *>(p)[i];
 }
 
-template <typename T, typename DT, int N>
-__global__ __launch_bounds__(64) void ssd_selective_scan_kernel(SelectiveArgs a) {
-    constexpr int NB = N / 4;   // states of a lane
+// ---------------------------------------------------------------------------
+// Scan. A workgroup owns 16 channels of one sequence; its TW waves take
+// segments of SEG tokens in turn (wave w: segments w, w + TW, ...). A
+// segment is an affine map of the state, h -> P h + e, and only that map's use
+// is serial:
+//   pass 1 (any time): the decays a_t = 2^(delta_t A log2 e), kept in registers,
+//     and e, the state after the segment from a zero state; P = 2^(A log2 e sum delta_t);
+//   chain (in order): wait for the state h_in that enters the segment, publish
+//     P h_in + e for the next segment's wave;
+//   pass 2: h_t = a_t h_(t-1) + b_t again from h_in, and y_t = h_t . C_t.
+// The exponentials, which cost most, are computed once; the price of running
+// TW segments side by side is one product and the outer product b_t a second
+// time. The chain runs through LDS: one state buffer, which each segment's wave
+// reads and then overwrites, and a counter of finished segments.
+//
+// Lanes: lane = 16 q + c holds the states n = 16 nb + 4 q + i (i < 4) of channel
+// c, for one block nb of 16 states at a time. b_t = (delta_t u_t) B_t is an
+// outer product of 16 channels and 16 states: one v_mfma_f32_4x4x1 (16 blocks
+// of 4x4; lane l gives B_t[4 q + l % 4] and delta_t u_t of its channel, and
+// receives the four b of its own states on top of the a h it passes as the sum).
+// What is per (token, channel) only - softplus, gate, loads, stores - is done
+// by lane (q, c) for the tokens 4 j + q, so nothing is computed four times;
+// delta and delta u reach the other lanes through LDS, and the four partial
+// sums of y_t come back by three half swaps per four tokens.
+constexpr int kCh = 16;    // channels of a workgroup
+
+template <typename T> struct RawOf;
+template <> struct RawOf<__bf16> {
+    using One = uint16_t;
+    struct __attribute__((packed, aligned(2))) Four { uint32_t w[2]; };
+    __device__ static float f(One v) { return __uint_as_float((uint32_t)v << 16); }
+    __device__ static f32x4 f4(const Four &v) {
+        return f32x4{bf16_lo(v.w[0]), bf16_hi(v.w[0]), bf16_lo(v.w[1]), bf16_hi(v.w[1])};
+    }
+};
+template <> struct RawOf<float> {
+    using One = float;
+    struct __attribute__((packed, aligned(4))) Four { float w[4]; };
+    __device__ static float f(One v) { return v; }
+    __device__ static f32x4 f4(const Four &v) { return f32x4{v.w[0], v.w[1], v.w[2], v.w[3]}; }
+};
+
+// Rows of a (tokens, row) tensor: a uniform address per token run plus 32-bit lane offsets (row_stride() of the API
+// bounds 16 rows below 2^34 bytes, 4 rows below 2^32).
+template <typename One> struct Rows {
+    const char *base;      // element 0 of the run's first row
+    int64_t step;          // bytes between rows
+    __device__ Rows(const void *p, int64_t first, int64_t stride)
+        : base(reinterpret_cast<const char *>(p) + first * stride * (int64_t)sizeof(One)),
+          step(stride * (int64_t)sizeof(One)) {}
+    // row 4 j + q, column bytes in `off` = q step + column bytes
+    __device__ One at(int j, uint32_t off) const {
+        return *reinterpret_cast<const One *>(base + 4 * j * step + off);
+    }
+    // any row
+    __device__ One row(int r, uint32_t col) const {
+        return *reinterpret_cast<const One *>(base + (int64_t)r * step + col);
+    }
+};
+
+// Sums of y_j (j < 4) over the four lanes 16 apart: lane (q, c) gets that of y_q.
+__device__ __forceinline__ float sum_scatter4(const float (&y)[4]) {
+    auto swap32 = [](float a, float b) {   // [a.lo | b.lo] + [a.hi | b.hi]
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+        return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    };
+    const float r0 = swap32(y[0], y[2]), r1 = swap32(y[1], y[3]);
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(r0), __float_as_uint(r1), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+template <typename T, typename DT, int N, int SEG>
+__global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs a) {
+    constexpr int NBLK = N / 16, J = SEG / 4;
+    using R = RawOf<T>;
+    using RD = RawOf<DT>;
+    using One = typename R::One;
+    using OneD = typename RD::One;
+    using Four = typename R::Four;
+    extern __shared__ __attribute__((aligned(16))) float lds[];
     if (__builtin_nontemporal_load(a.error_flag) & SSD_DATA_BAD_CU_SEQLENS) return;
-    const int cblocks = (a.C_total + 15) / 16;
-    const int rank = blockIdx.x / cblocks, cb = blockIdx.x - rank * cblocks;
+    const int per = a.C_total / a.G, bpg = (per + kCh - 1) / kCh, cblocks = a.G * bpg;   // blocks stay inside a group
+    // four neighbouring channel blocks (one 128-byte line of bf16) on one XCD
+    const int total = (int)gridDim.x;
+    int b = blockIdx.x;
+    if ((b | 31) < total) b = (b & ~31) | ((b & 7) << 2) | ((b >> 3) & 3);
+    const int rank = b / cblocks, cb = b - rank * cblocks;
     const int s = a.seq_order[rank];
     if (s < 0 || s >= a.S) return;
     int64_t tb = a.cu_seqlens[s], te = a.cu_seqlens[s + 1];
     tb = tb < 0 ? 0 : (tb > a.T ? a.T : tb);
     te = te < tb ? tb : (te > a.T ? a.T : te);
     const int L = (int)(te - tb), c0 = a.seq_chunk_start[s];
-    const int lane = threadIdx.x, q = lane >> 4, ch = cb * 16 + (lane & 15);
-    const bool live = ch < a.C_total;
-    const int d = live ? ch : a.C_total - 1;
-    const int g = d / (a.C_total / a.G);
-    const int64_t row = ((int64_t)s * a.C_total + d) * N + q * NB;
+    const int nseg = (L + SEG - 1) / SEG, nw = (int)blockDim.x >> 6;
 
-    float h[NB], a2[NB];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int q = lane >> 4, c = lane & 15, g = cb / bpg, ch = (cb - g * bpg) * kCh + c;
+    const bool live = ch < per;
+    const int d = g * per + (live ? ch : per - 1);
+
+    float *carry = lds;                                           // [NBLK][64][4]
+    volatile int *done = reinterpret_cast<volatile int *>(lds + NBLK * 256);   // [NBLK] segments finished
+    float *mine = lds + NBLK * 256 + ((NBLK + 3) & ~3) + wave * (SEG * 64);
+    float *ldsD = mine;                 // [SEG tokens][16 channels] (delta, delta u)
+    float *ldsB = mine + SEG * 32;      // [SEG tokens][16 states]
+    float *ldsC = mine + SEG * 48;
+
+    const int64_t state_row = (int64_t)s * a.C_total * N + (int64_t)d * N + 4 * q;
     const bool start = a.init != nullptr && (a.has_init == nullptr || a.has_init[s] != 0);
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-        a2[i] = a.A[(int64_t)d * N + q * NB + i] * kLog2e;
-        h[i] = start ? a.init[row + i] : 0.0f;
+    for (int nb = wave; nb < NBLK; nb += nw) {
+        const f32x4 h = start ? *reinterpret_cast<const f32x4 *>(a.init + state_row + nb * 16) : f32x4{0, 0, 0, 0};
+        *reinterpret_cast<f32x4 *>(carry + (nb * 64 + lane) * 4) = h;
+        if (nseg == 0 && live) *reinterpret_cast<f32x4 *>(a.final_states + state_row + nb * 16) = h;
+        if (lane == 0) done[nb] = 0;
     }
+    __syncthreads();
+
     const float bias = a.dt_bias != nullptr ? a.dt_bias[d] : 0.0f, skip = a.D != nullptr ? a.D[d] : 0.0f;
-    for (int t = 0; t < L; ++t) {
-        const int64_t tok = tb + t;
-        const float u = load_f<T>(a.u, tok * a.u_stride + d);
-        const float delta = softplus_full(load_f<DT>(a.dt, tok * a.dt_stride + d) + bias);
-        const float du = delta * u;
-        float y = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const int n = g * N + q * NB + i;
-            h[i] = fmaf(fast_exp2(delta * a2[i]), h[i], du * load_f<T>(a.B, tok * a.B_stride + n));
-            y = fmaf(h[i], load_f<T>(a.C, tok * a.C_stride + n), y);
+    f32x4 rate = *reinterpret_cast<const f32x4 *>(a.A + (int64_t)d * N + 4 * q) * kLog2e;
+    const uint32_t colT = d * sizeof(One), colD = d * sizeof(OneD);
+    const uint32_t offU = q * (uint32_t)a.u_stride * (uint32_t)sizeof(One) + colT;
+    const uint32_t offD = q * (uint32_t)a.dt_stride * (uint32_t)sizeof(OneD) + colD;
+    const uint32_t offZ = q * (uint32_t)a.z_stride * (uint32_t)sizeof(One) + colT;
+
+    // raw inputs of a segment, fetched one segment ahead: tokens 4 j + q of channel c; four states of B and C of one
+    // token (SEG = 8: lanes 0 .. 31 hold B, the others C; SEG = 16: every lane holds both)
+    One ru[J];
+    OneD rd[J];
+    Four rB, rC;
+    auto fetch_bc = [&](int seg, int nb) {
+        const int r = min((lane >> 2) & (SEG - 1), L - 1 - seg * SEG);
+        const uint32_t col = (g * N + nb * 16 + 4 * (lane & 3)) * (uint32_t)sizeof(One);
+        const int64_t first = tb + seg * SEG;
+        if constexpr (SEG == 16) {
+            const Rows<One> rows_b(a.B, first, a.B_stride), rows_c(a.C, first, a.C_stride);
+            rB = *reinterpret_cast<const Four *>(rows_b.base + r * rows_b.step + col);
+            rC = *reinterpret_cast<const Four *>(rows_c.base + r * rows_c.step + col);
+        } else {
+            const Rows<One> rows(lane < 32 ? a.B : a.C, first, lane < 32 ? a.B_stride : a.C_stride);
+            rB = *reinterpret_cast<const Four *>(rows.base + r * rows.step + col);
         }
-        y += __shfl_xor(y, 16);
-        y += __shfl_xor(y, 32);
-        y = fmaf(skip, u, y);
-        if (a.z != nullptr) y *= silu_full(load_f<T>(a.z, tok * a.z_stride + d));
-        if (live && q == 0) reinterpret_cast<T *>(a.y)[tok * a.y_stride + d] = (T)y;
-        if (a.chunk_states != nullptr && ((t + 1) % a.cs == 0 || t + 1 == L)) {
-            const int chunk = c0 + t / a.cs;
-            const int slot = a.chunk_state_dst != nullptr ? a.chunk_state_dst[chunk] : chunk;
-            if (slot >= a.capacity) {
-                if (lane == 0 && cb == 0) atomicOr(a.error_flag, SSD_DATA_BAD_SLOT);
-            } else if (slot >= 0 && live) {
+    };
+    auto fetch = [&](int seg) {
+        const Rows<One> rows_u(a.u, tb + seg * SEG, a.u_stride);
+        const Rows<OneD> rows_d(a.dt, tb + seg * SEG, a.dt_stride);
+        const int last = L - 1 - seg * SEG;
+        if (last >= SEG - 1) {
 #pragma unroll
-                for (int i = 0; i < NB; ++i)
-                    a.chunk_states[((int64_t)slot * a.C_total + d) * N + q * NB + i] = h[i];
+            for (int j = 0; j < J; ++j) {
+                ru[j] = rows_u.at(j, offU);
+                rd[j] = rows_d.at(j, offD);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int r = min(4 * j + q, last);
+                ru[j] = rows_u.row(r, colT);
+                rd[j] = rows_d.row(r, colD);
             }
         }
-    }
-    if (live)
+        fetch_bc(seg, 0);
+    };
+    if (wave < nseg) fetch(wave);
+
+    for (int seg = wave; seg < nseg; seg += nw) {
+        const int left = L - seg * SEG;   // tokens from the segment's first on
+        // the slot that receives the state after this segment, if a chunk ends here
+        int slot = -1;
+        if (a.chunk_states != nullptr && (left <= SEG || ((seg + 1) * SEG) % a.cs == 0)) {
+            const int chunk = c0 + (seg * SEG) / a.cs;
+            slot = a.chunk_state_dst != nullptr ? a.chunk_state_dst[chunk] : chunk;
+            if (slot >= a.capacity) {
+                if (cb == 0 && lane == 0) atomicOr(a.error_flag, SSD_DATA_BAD_SLOT);
+                slot = -1;
+            }
+        }
+        // gate inputs: used at the segment's end only
+        One rz[J];
+        if (a.z != nullptr) {
+            const Rows<One> rows_z(a.z, tb + seg * SEG, a.z_stride);
 #pragma unroll
-        for (int i = 0; i < NB; ++i) a.final_states[row + i] = h[i];
+            for (int j = 0; j < J; ++j)
+                rz[j] = left >= SEG ? rows_z.at(j, offZ) : rows_z.row(min(4 * j + q, left - 1), colT);
+        }
+        float u[J], sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            u[j] = R::f(ru[j]);
+            const bool in = 4 * j + q < left;
+            const float delta = in ? softplus_full(RD::f(rd[j]) + bias) : 0.0f;
+            sum += delta;
+            *reinterpret_cast<f32x2 *>(ldsD + ((4 * j + q) * 16 + c) * 2) = f32x2{delta, in ? delta * u[j] : 0.0f};
+        }
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+
+        const Rows<One> rows_y(a.y, tb + seg * SEG, a.y_stride);
+        auto emit = [&](int j, const float (&part)[4]) {   // tokens 4 j .. 4 j + 3
+            float v = fmaf(skip, u[j], sum_scatter4(part));
+            if (a.z != nullptr) v *= silu_full(R::f(rz[j]));
+            if (live && 4 * j + q < left)
+                *reinterpret_cast<T *>(const_cast<char *>(rows_y.base) + (4 * j + q) * rows_y.step + colT) = (T)v;
+        };
+        float y[NBLK > 1 ? SEG : 4];
+        if constexpr (NBLK > 1) {
+#pragma unroll
+            for (int t = 0; t < SEG; ++t) y[t] = 0.0f;
+        }
+
+#pragma unroll 1
+        for (int nb = 0; nb < NBLK; ++nb) {
+            if constexpr (SEG == 16) {
+                *reinterpret_cast<f32x4 *>(ldsB + lane * 4) = R::f4(rB);
+                *reinterpret_cast<f32x4 *>(ldsC + lane * 4) = R::f4(rC);
+            } else {
+                *reinterpret_cast<f32x4 *>(ldsB + lane * 4) = R::f4(rB);   // C follows B
+            }
+            if (NBLK > 1) rate = *reinterpret_cast<const f32x4 *>(a.A + (int64_t)d * N + nb * 16 + 4 * q) * kLog2e;
+            if (nb + 1 < NBLK) fetch_bc(seg, nb + 1);
+            else if (seg + nw < nseg) fetch(seg + nw);
+            __builtin_amdgcn_wave_barrier();
+
+            f32x4 dec[SEG], h = {0, 0, 0, 0};
+#pragma unroll
+            for (int t = 0; t < SEG; ++t) {
+                const f32x2 dd = *reinterpret_cast<const f32x2 *>(ldsD + (t * 16 + c) * 2);
+                const float bt = ldsB[t * 16 + 4 * q + (lane & 3)];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    dec[t][i] = fast_exp2(dd[0] * rate[i]);
+                    h[i] *= dec[t][i];
+                }
+                h = __builtin_amdgcn_mfma_f32_4x4x1f32(bt, dd[1], h, 0, 0, 0);
+                if (t % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // bounds the LDS reads in flight, so the registers
+            }
+            f32x4 p;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = fast_exp2(sum * rate[i]);
+
+            // the chain: segment seg's wave is the only one that touches the buffer between done = seg and seg + 1
+            float *slot_lds = carry + (nb * 64 + lane) * 4;
+            while (__builtin_amdgcn_readfirstlane(done[nb]) < seg) __builtin_amdgcn_s_sleep(1);
+            asm volatile("" ::: "memory");
+            f32x4 in = *reinterpret_cast<const f32x4 *>(slot_lds);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = fmaf(p[i], in[i], h[i]);
+            *reinterpret_cast<f32x4 *>(slot_lds) = h;
+            asm volatile("" ::: "memory");
+            if (lane == 0) done[nb] = seg + 1;   // LDS operations of a wave take effect in order
+            asm volatile("" ::: "memory");
+            if (live) {
+                if (slot >= 0)
+                    *reinterpret_cast<f32x4 *>(a.chunk_states + ((int64_t)slot * a.C_total + d) * N + nb * 16 + 4 * q) = h;
+                if (left <= SEG) *reinterpret_cast<f32x4 *>(a.final_states + state_row + nb * 16) = h;
+            }
+
+#pragma unroll
+            for (int t = 0; t < SEG; ++t) {
+                const float du = ldsD[(t * 16 + c) * 2 + 1];
+                const float bt = ldsB[t * 16 + 4 * q + (lane & 3)];
+                const f32x4 cv = *reinterpret_cast<const f32x4 *>(ldsC + t * 16 + 4 * q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) in[i] *= dec[t][i];
+                in = __builtin_amdgcn_mfma_f32_4x4x1f32(bt, du, in, 0, 0, 0);
+                float v = NBLK > 1 ? y[NBLK > 1 ? t : 0] : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v = fmaf(in[i], cv[i], v);
+                y[NBLK > 1 ? t : t & 3] = v;
+                if constexpr (NBLK == 1) {
+                    if (t % 4 == 3) emit(t / 4, {y[0], y[1], y[2], y[3]});
+                }
+                if (t % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+        if constexpr (NBLK > 1) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) emit(j, {y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]});
+        }
+    }
 }
+
+// Waves of a scan workgroup
+static int selective_waves(int64_t chains) { return chains >= 1024 ? 4 : chains >= 512 ? 8 : 16; }
 
 // Step: lanes own 4 consecutive states of one channel (N / 4 lanes a channel).
 constexpr int kSelStepThreads = 256;
@@ -139,8 +369,13 @@ __global__ __launch_bounds__(kSelStepThreads) void ssd_selective_step_kernel(Sel
 
 template <typename T, typename DT, int N> struct SelectiveLaunch {
     static hipError_t scan(const SelectiveArgs &a, hipStream_t stream) {
-        const int64_t blocks = (int64_t)a.S * ((a.C_total + 15) / 16);
-        hipLaunchKernelGGL((ssd_selective_scan_kernel<T, DT, N>), dim3((unsigned)blocks), dim3(64), 0, stream, a);
+        const int64_t blocks = (int64_t)a.S * a.G * ((a.C_total / a.G + kCh - 1) / kCh);
+        const int waves = selective_waves(blocks);
+        constexpr int NBLK = N / 16;
+        constexpr int SEG = SEL_SEG;
+        const size_t lds = sizeof(float) * (NBLK * 256 + ((NBLK + 3) & ~3) + (size_t)waves * SEG * 64);
+        hipLaunchKernelGGL((ssd_selective_scan_kernel<T, DT, N, SEG>), dim3((unsigned)blocks), dim3(64 * waves), lds, stream,
+                           a);
         return hipGetLastError();
     }
     static hipError_t step(const SelectiveArgs &a, hipStream_t stream) {
