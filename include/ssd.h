@@ -389,7 +389,7 @@ ssd_status ssd_causal_conv1d_varlen(
  *  dt_bias, D      float32 (channels) or NULL (= 0)
  *  A               float32 (channels, dstate)
  *  *_stride        elements from one token's row to the next (rows themselves
- *                  are contiguous): at least the row's length, at most 2^28.
+ *                  are contiguous): at least the row's length, at most 2^26.
  *                  So halves of one projection's output are passed as they are.
  *  initial_states, final_states  float32 (S, channels, dstate)
  *  chunk_states    optional state export after each chunk of meta's grid, as
@@ -443,7 +443,7 @@ ssd_status ssd_selective_step(
  * ends with the token, goes to conv_states[write_slot[s]] (skipped when < 0).
  *  x, out          element type `in_dtype`, (nseqs, channels), rows x_stride /
  *                  out_stride elements apart (multiples of 8, at least
- *                  channels, at most 2^28), 16-byte aligned
+ *                  channels, at most 2^26), 16-byte aligned
  *  weight, bias, conv_states, channels, width, activation  as for
  *                  ssd_causal_conv1d_varlen
  *  read_slot, write_slot  int32 (nseqs) or NULL (= all -1). Equal slots update
@@ -478,7 +478,7 @@ typedef enum {
  *     out = (v - mu) / sqrt(mean((v - mu)^2) + eps) * weight[c] + bias[c]
  * then the activation. Scan outputs (T, H, P) are rows of H*P channels.
  *  x, z, out       element type `in_dtype`, (rows, channels), rows *_stride
- *                  elements apart (at least channels, at most 2^28); z is read
+ *                  elements apart (at least channels, at most 2^26); z is read
  *                  only by the gated forms. out may be x itself.
  *  weight, bias    float32 (channels) or NULL (= 1, 0)
  * Supported: any channels % ngroups == 0 with groups of at most 16384

@@ -30,8 +30,8 @@ bool known_dtype(ssd_dtype t) { return t == SSD_F32 || t == SSD_BF16; }
 uintptr_t elem_bytes(ssd_dtype t) { return t == SSD_BF16 ? 2 : 4; }
 
 // Rows of `row` contiguous elements, `stride` elements apart. The bound keeps
-// every byte offset inside a few rows below 2^32.
-bool row_stride(int64_t stride, int64_t row) { return stride >= row && stride <= (int64_t(1) << 28); }
+// every byte offset inside 16 rows below 2^32.
+bool row_stride(int64_t stride, int64_t row) { return stride >= row && stride <= (int64_t(1) << 26); }
 
 // What the selective scan and its step ask of their shared arguments.
 ssd_status check_selective(const ssd::SelectiveArgs &a, ssd_dtype in_dtype, ssd_dtype dt_dtype, bool rows) {
@@ -42,7 +42,7 @@ ssd_status check_selective(const ssd::SelectiveArgs &a, ssd_dtype in_dtype, ssd_
     if (rows && (a.u == nullptr || a.dt == nullptr || a.B == nullptr || a.C == nullptr || a.y == nullptr))
         return SSD_ERR_NULL_ARG;
     const int64_t C = a.C_total, GN = (int64_t)a.G * a.N;
-    if (GN > (int64_t(1) << 28)) return SSD_ERR_SHAPE;
+    if (GN > (int64_t(1) << 26) || C > (int64_t(1) << 26)) return SSD_ERR_SHAPE;
     if (rows && (!row_stride(a.u_stride, C) || !row_stride(a.dt_stride, C) || !row_stride(a.y_stride, C) ||
                  !row_stride(a.B_stride, GN) || !row_stride(a.C_stride, GN) ||
                  (a.z != nullptr && !row_stride(a.z_stride, C))))

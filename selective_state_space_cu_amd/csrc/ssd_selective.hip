@@ -9,6 +9,8 @@
 //
 // Lanes: a wave owns 16 channels; lane = 16 q + c holds the states
 // n = q N/4 .. (q + 1) N/4 - 1 of channel c.
+#include <type_traits>
+
 #include "ssd_scan.hpp"
 #ifndef SEL_SEG
 #define SEL_SEG 8
@@ -18,19 +20,21 @@ namespace ssd {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-// log(1 + e^v) in float32. For small e^v the logarithm's own argument 1 + e^v
-// has lost the digits that count, so its series is summed instead
-// (z <= 1/8: the first term left out is below z^7/8 = 6e-8 of the result).
+// log(1 + e^v) = max(v, 0) + log1p(z), z = e^-|v| in (0, 1]. log1p(z) / z is a
+// polynomial of degree 8 fitted over all of (0, 1] for the least relative error
+// (with the roundings of its evaluation at most 3.2 * 2^-24): the hardware's
+// logarithm of 1 + z has lost the digits of a small z, and costs as much as three sums.
 __device__ __forceinline__ float softplus_full(float v) {
     const float z = fast_exp2(-fabsf(v) * kLog2e);
-    const float big = __builtin_amdgcn_logf(1.0f + z) * 0.6931471805599453f;
-    float p = fmaf(z, 1.0f / 7.0f, -1.0f / 6.0f);
-    p = fmaf(z, p, 1.0f / 5.0f);
-    p = fmaf(z, p, -1.0f / 4.0f);
-    p = fmaf(z, p, 1.0f / 3.0f);
-    p = fmaf(z, p, -1.0f / 2.0f);
+    float p = fmaf(z, 0.0052319662645459175f, -0.029502321034669876f);
+    p = fmaf(z, p, 0.07822119444608688f);
+    p = fmaf(z, p, -0.1366284191608429f);
+    p = fmaf(z, p, 0.1910581737756729f);
+    p = fmaf(z, p, -0.2484293431043625f);
+    p = fmaf(z, p, 0.33319091796875f);
+    p = fmaf(z, p, -0.4999949336051941f);
     p = fmaf(z, p, 1.0f);
-    return fmaxf(v, 0.0f) + (z <= 0.125f ? z * p : big);
+    return fmaf(z, p, fmaxf(v, 0.0f));
 }
 
 __device__ __forceinline__ float silu_full(float v) {
@@ -83,24 +87,6 @@ template <> struct RawOf<float> {
     __device__ static f32x4 f4(const Four &v) { return f32x4{v.w[0], v.w[1], v.w[2], v.w[3]}; }
 };
 
-// Rows of a (tokens, row) tensor: a uniform address per token run plus 32-bit lane offsets (row_stride() of the API
-// bounds 16 rows below 2^34 bytes, 4 rows below 2^32).
-template <typename One> struct Rows {
-    const char *base;      // element 0 of the run's first row
-    int64_t step;          // bytes between rows
-    __device__ Rows(const void *p, int64_t first, int64_t stride)
-        : base(reinterpret_cast<const char *>(p) + first * stride * (int64_t)sizeof(One)),
-          step(stride * (int64_t)sizeof(One)) {}
-    // row 4 j + q, column bytes in `off` = q step + column bytes
-    __device__ One at(int j, uint32_t off) const {
-        return *reinterpret_cast<const One *>(base + 4 * j * step + off);
-    }
-    // any row
-    __device__ One row(int r, uint32_t col) const {
-        return *reinterpret_cast<const One *>(base + (int64_t)r * step + col);
-    }
-};
-
 // Sums of y_j (j < 4) over the four lanes 16 apart: lane (q, c) gets that of y_q.
 __device__ __forceinline__ float sum_scatter4(const float (&y)[4]) {
     auto swap32 = [](float a, float b) {   // [a.lo | b.lo] + [a.hi | b.hi]
@@ -112,6 +98,14 @@ __device__ __forceinline__ float sum_scatter4(const float (&y)[4]) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// Sum over the four lanes 16 apart; every lane gets it.
+__device__ __forceinline__ float sum_lanes4(float v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
 template <typename T, typename DT, int N, int SEG>
 __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs a) {
     constexpr int NBLK = N / 16, J = SEG / 4;
@@ -120,6 +114,7 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
     using One = typename R::One;
     using OneD = typename RD::One;
     using Four = typename R::Four;
+    typedef __attribute__((address_space(3))) volatile int lds_counter;   // (a generic pointer's access waits for all loads)
     extern __shared__ __attribute__((aligned(16))) float lds[];
     if (__builtin_nontemporal_load(a.error_flag) & SSD_DATA_BAD_CU_SEQLENS) return;
     const int per = a.C_total / a.G, bpg = (per + kCh - 1) / kCh, cblocks = a.G * bpg;   // blocks stay inside a group
@@ -135,6 +130,7 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
     te = te < tb ? tb : (te > a.T ? a.T : te);
     const int L = (int)(te - tb), c0 = a.seq_chunk_start[s];
     const int nseg = (L + SEG - 1) / SEG, nw = (int)blockDim.x >> 6;
+    const int chunk_segs = a.cs / SEG, chunk_shift = __builtin_ctz(chunk_segs);
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q = lane >> 4, c = lane & 15, g = cb / bpg, ch = (cb - g * bpg) * kCh + c;
@@ -142,107 +138,114 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
     const int d = g * per + (live ? ch : per - 1);
 
     float *carry = lds;                                           // [NBLK][64][4]
-    volatile int *done = reinterpret_cast<volatile int *>(lds + NBLK * 256);   // [NBLK] segments finished
+    lds_counter *done = (lds_counter *)(__attribute__((address_space(3))) int *)(lds + NBLK * 256);   // [NBLK] segments finished
     float *mine = lds + NBLK * 256 + ((NBLK + 3) & ~3) + wave * (SEG * 64);
     float *ldsD = mine;                 // [SEG tokens][16 channels] (delta, delta u)
     float *ldsB = mine + SEG * 32;      // [SEG tokens][16 states]
     float *ldsC = mine + SEG * 48;
 
-    const int64_t state_row = (int64_t)s * a.C_total * N + (int64_t)d * N + 4 * q;
+    const int64_t state_row = (int64_t)s * a.C_total * N;
+    const int64_t state_col = (int64_t)d * N + 4 * q;
+    float *final = a.final_states + state_row;
     const bool start = a.init != nullptr && (a.has_init == nullptr || a.has_init[s] != 0);
     for (int nb = wave; nb < NBLK; nb += nw) {
-        const f32x4 h = start ? *reinterpret_cast<const f32x4 *>(a.init + state_row + nb * 16) : f32x4{0, 0, 0, 0};
+        const f32x4 h = start ? *reinterpret_cast<const f32x4 *>(a.init + state_row + nb * 16 + state_col) : f32x4{0, 0, 0, 0};
         *reinterpret_cast<f32x4 *>(carry + (nb * 64 + lane) * 4) = h;
-        if (nseg == 0 && live) *reinterpret_cast<f32x4 *>(a.final_states + state_row + nb * 16) = h;
+        if (nseg == 0 && live) *reinterpret_cast<f32x4 *>(final + nb * 16 + state_col) = h;
         if (lane == 0) done[nb] = 0;
     }
     __syncthreads();
+    if (wave >= nseg) return;
 
     const float bias = a.dt_bias != nullptr ? a.dt_bias[d] : 0.0f, skip = a.D != nullptr ? a.D[d] : 0.0f;
     f32x4 rate = *reinterpret_cast<const f32x4 *>(a.A + (int64_t)d * N + 4 * q) * kLog2e;
-    const uint32_t colT = d * sizeof(One), colD = d * sizeof(OneD);
-    const uint32_t offU = q * (uint32_t)a.u_stride * (uint32_t)sizeof(One) + colT;
-    const uint32_t offD = q * (uint32_t)a.dt_stride * (uint32_t)sizeof(OneD) + colD;
-    const uint32_t offZ = q * (uint32_t)a.z_stride * (uint32_t)sizeof(One) + colT;
+
+    // Addresses: uniform pointers to the first row of a segment, advanced from segment to segment, plus 32-bit lane
+    // offsets (the API's bound on strides keeps 16 rows below 2^32 bytes).
+    constexpr int ES = sizeof(One), ED = sizeof(OneD);
+    const int64_t first = tb + wave * SEG;
+    const int64_t su = a.u_stride * ES, sd = a.dt_stride * ED, sz = (a.z ? a.z_stride : a.u_stride) * ES, sy = a.y_stride * ES,
+                  sB = a.B_stride * ES, sC = a.C_stride * ES;
+    const char *pu = reinterpret_cast<const char *>(a.u) + first * su, *pd = reinterpret_cast<const char *>(a.dt) + first * sd;
+    const char *pz = reinterpret_cast<const char *>(a.z ? a.z : a.u) + first * sz;   // (no gate: loaded again, unused)
+    char *py = reinterpret_cast<char *>(a.y) + first * sy;
+    const uint32_t offU = q * (uint32_t)su + d * ES, offD = q * (uint32_t)sd + d * ED, offZ = q * (uint32_t)sz + d * ES,
+                   offY = q * (uint32_t)sy + d * ES;
+    // B and C: every lane its own token and four states, through a pointer of its own
+    const int tokBC = lane >> 2 & (SEG - 1);
+    const bool holdsB = SEG == 16 || lane < 32;
+    const int64_t sBC = holdsB ? sB : sC;
+    const char *pBC = (holdsB ? reinterpret_cast<const char *>(a.B) : reinterpret_cast<const char *>(a.C)) +
+                      (first + tokBC) * sBC + (g * N + 4 * (lane & 3)) * ES;
+    const char *pC = SEG == 16 ? reinterpret_cast<const char *>(a.C) + (first + tokBC) * sC + (g * N + 4 * (lane & 3)) * ES
+                               : nullptr;
+
+    // bytes from a wave's segment to its next
+    const int64_t ahead = (int64_t)nw * SEG, nextU = ahead * su, nextD = ahead * sd, nextZ = ahead * sz, nextY = ahead * sy,
+                  nextBC = ahead * sBC, nextC = ahead * sC;
 
     // raw inputs of a segment, fetched one segment ahead: tokens 4 j + q of channel c; four states of B and C of one
-    // token (SEG = 8: lanes 0 .. 31 hold B, the others C; SEG = 16: every lane holds both)
-    One ru[J];
+    // token (SEG = 8: 32 lanes hold B, the others C; SEG = 16: every lane holds both)
+    One ru[J], rz[J];
     OneD rd[J];
     Four rB, rC;
-    auto fetch_bc = [&](int seg, int nb) {
-        const int r = min((lane >> 2) & (SEG - 1), L - 1 - seg * SEG);
-        const uint32_t col = (g * N + nb * 16 + 4 * (lane & 3)) * (uint32_t)sizeof(One);
-        const int64_t first = tb + seg * SEG;
-        if constexpr (SEG == 16) {
-            const Rows<One> rows_b(a.B, first, a.B_stride), rows_c(a.C, first, a.C_stride);
-            rB = *reinterpret_cast<const Four *>(rows_b.base + r * rows_b.step + col);
-            rC = *reinterpret_cast<const Four *>(rows_c.base + r * rows_c.step + col);
-        } else {
-            const Rows<One> rows(lane < 32 ? a.B : a.C, first, lane < 32 ? a.B_stride : a.C_stride);
-            rB = *reinterpret_cast<const Four *>(rows.base + r * rows.step + col);
-        }
+    auto fetch_bc = [&](int rows, int nb) {   // rows past the end: the last one
+        const int64_t back = max(tokBC - (rows - 1), 0);
+        rB = *reinterpret_cast<const Four *>(pBC + nb * 16 * ES - (rows >= SEG ? 0 : back * sBC));
+        if constexpr (SEG == 16) rC = *reinterpret_cast<const Four *>(pC + nb * 16 * ES - (rows >= SEG ? 0 : back * sC));
     };
-    auto fetch = [&](int seg) {
-        const Rows<One> rows_u(a.u, tb + seg * SEG, a.u_stride);
-        const Rows<OneD> rows_d(a.dt, tb + seg * SEG, a.dt_stride);
-        const int last = L - 1 - seg * SEG;
-        if (last >= SEG - 1) {
+    auto fetch = [&] {   // a segment of SEG tokens
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                ru[j] = rows_u.at(j, offU);
-                rd[j] = rows_d.at(j, offD);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int r = min(4 * j + q, last);
-                ru[j] = rows_u.row(r, colT);
-                rd[j] = rows_d.row(r, colD);
-            }
+        for (int j = 0; j < J; ++j) {
+            ru[j] = *reinterpret_cast<const One *>(pu + 4 * j * su + offU);
+            rd[j] = *reinterpret_cast<const OneD *>(pd + 4 * j * sd + offD);
+            rz[j] = *reinterpret_cast<const One *>(pz + 4 * j * sz + offZ);
         }
-        fetch_bc(seg, 0);
+        fetch_bc(SEG, 0);
     };
-    if (wave < nseg) fetch(wave);
+    auto fetch_rest = [&](int rows) {   // a segment of fewer: past the end, the last token again
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const uint32_t r = min(4 * j + q, rows - 1);
+            ru[j] = *reinterpret_cast<const One *>(pu + (r * (uint32_t)su + d * ES));
+            rd[j] = *reinterpret_cast<const OneD *>(pd + (r * (uint32_t)sd + d * ED));
+            rz[j] = *reinterpret_cast<const One *>(pz + (r * (uint32_t)sz + d * ES));
+        }
+        fetch_bc(rows, 0);
+    };
+    if ((wave + 1) * SEG <= L) fetch();
 
-    for (int seg = wave; seg < nseg; seg += nw) {
-        const int left = L - seg * SEG;   // tokens from the segment's first on
+    auto segment = [&](int seg, auto whole) {
+        constexpr bool FULL = decltype(whole)::value;   // all SEG tokens exist
+        const int left = L - seg * SEG;                 // tokens from the segment's first on
+        if constexpr (!FULL) fetch_rest(left);          // once a sequence: not ahead
         // the slot that receives the state after this segment, if a chunk ends here
         int slot = -1;
-        if (a.chunk_states != nullptr && (left <= SEG || ((seg + 1) * SEG) % a.cs == 0)) {
-            const int chunk = c0 + (seg * SEG) / a.cs;
-            slot = a.chunk_state_dst != nullptr ? a.chunk_state_dst[chunk] : chunk;
+        if (a.chunk_states != nullptr && (!FULL || left == SEG || ((seg + 1) & (chunk_segs - 1)) == 0)) {
+            const int chunk = c0 + (seg >> chunk_shift);
+            slot = __builtin_amdgcn_readfirstlane(a.chunk_state_dst != nullptr ? a.chunk_state_dst[chunk] : chunk);
             if (slot >= a.capacity) {
                 if (cb == 0 && lane == 0) atomicOr(a.error_flag, SSD_DATA_BAD_SLOT);
                 slot = -1;
             }
         }
-        // gate inputs: used at the segment's end only
-        One rz[J];
-        if (a.z != nullptr) {
-            const Rows<One> rows_z(a.z, tb + seg * SEG, a.z_stride);
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-                rz[j] = left >= SEG ? rows_z.at(j, offZ) : rows_z.row(min(4 * j + q, left - 1), colT);
-        }
         float u[J], sum = 0.0f;
+        One z[J];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             u[j] = R::f(ru[j]);
-            const bool in = 4 * j + q < left;
-            const float delta = in ? softplus_full(RD::f(rd[j]) + bias) : 0.0f;
+            z[j] = rz[j];
+            float delta = softplus_full(RD::f(rd[j]) + bias), du = delta * u[j];
+            if (!FULL && 4 * j + q >= left) delta = du = 0.0f;
             sum += delta;
-            *reinterpret_cast<f32x2 *>(ldsD + ((4 * j + q) * 16 + c) * 2) = f32x2{delta, in ? delta * u[j] : 0.0f};
+            *reinterpret_cast<f32x2 *>(ldsD + ((4 * j + q) * 16 + c) * 2) = f32x2{delta, du};
         }
-        sum += __shfl_xor(sum, 16);
-        sum += __shfl_xor(sum, 32);
+        sum = sum_lanes4(sum);
 
-        const Rows<One> rows_y(a.y, tb + seg * SEG, a.y_stride);
         auto emit = [&](int j, const float (&part)[4]) {   // tokens 4 j .. 4 j + 3
             float v = fmaf(skip, u[j], sum_scatter4(part));
-            if (a.z != nullptr) v *= silu_full(R::f(rz[j]));
-            if (live && 4 * j + q < left)
-                *reinterpret_cast<T *>(const_cast<char *>(rows_y.base) + (4 * j + q) * rows_y.step + colT) = (T)v;
+            if (a.z != nullptr) v *= silu_full(R::f(z[j]));
+            if (live && (FULL || 4 * j + q < left)) *reinterpret_cast<T *>(py + 4 * j * sy + offY) = (T)v;
         };
         float y[NBLK > 1 ? SEG : 4];
         if constexpr (NBLK > 1) {
@@ -252,15 +255,19 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
 
 #pragma unroll 1
         for (int nb = 0; nb < NBLK; ++nb) {
-            if constexpr (SEG == 16) {
-                *reinterpret_cast<f32x4 *>(ldsB + lane * 4) = R::f4(rB);
-                *reinterpret_cast<f32x4 *>(ldsC + lane * 4) = R::f4(rC);
-            } else {
-                *reinterpret_cast<f32x4 *>(ldsB + lane * 4) = R::f4(rB);   // C follows B
-            }
+            *reinterpret_cast<f32x4 *>(ldsB + lane * 4) = R::f4(rB);   // (SEG = 8: C follows B)
+            if constexpr (SEG == 16) *reinterpret_cast<f32x4 *>(ldsC + lane * 4) = R::f4(rC);
             if (NBLK > 1) rate = *reinterpret_cast<const f32x4 *>(a.A + (int64_t)d * N + nb * 16 + 4 * q) * kLog2e;
-            if (nb + 1 < NBLK) fetch_bc(seg, nb + 1);
-            else if (seg + nw < nseg) fetch(seg + nw);
+            if (nb + 1 < NBLK) {
+                fetch_bc(FULL ? SEG : left, nb + 1);
+            } else if (FULL) {
+                pu += nextU;
+                pd += nextD;
+                pz += nextZ;
+                pBC += nextBC;
+                if (SEG == 16) pC += nextC;
+                if (left >= (nw + 1) * SEG) fetch();
+            }
             __builtin_amdgcn_wave_barrier();
 
             f32x4 dec[SEG], h = {0, 0, 0, 0};
@@ -271,7 +278,7 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     dec[t][i] = fast_exp2(dd[0] * rate[i]);
-                    h[i] *= dec[t][i];
+                    if (t > 0) h[i] *= dec[t][i];
                 }
                 h = __builtin_amdgcn_mfma_f32_4x4x1f32(bt, dd[1], h, 0, 0, 0);
                 if (t % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // bounds the LDS reads in flight, so the registers
@@ -279,22 +286,34 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
             f32x4 p;
 #pragma unroll
             for (int i = 0; i < 4; ++i) p[i] = fast_exp2(sum * rate[i]);
+            asm volatile("" : "+v"(p));        // before the wait, not after it
+            __builtin_amdgcn_s_setprio(2);     // the other waves wait for what follows
 
-            // the chain: segment seg's wave is the only one that touches the buffer between done = seg and seg + 1
-            float *slot_lds = carry + (nb * 64 + lane) * 4;
-            while (__builtin_amdgcn_readfirstlane(done[nb]) < seg) __builtin_amdgcn_s_sleep(1);
-            asm volatile("" ::: "memory");
-            f32x4 in = *reinterpret_cast<const f32x4 *>(slot_lds);
+            // the chain: segment seg's wave is the only one that touches the buffer between done = seg and seg + 1.
+            // LDS operations of a wave take effect in order: a state read after a counter that says so is that state
+            f32x4 *state = reinterpret_cast<f32x4 *>(carry + (nb * 64 + lane) * 4);
+            f32x4 in;
+            for (;;) {
+                const int n = done[nb];
+                asm volatile("" ::: "memory");
+                in = *state;
+                const int ahead = seg - __builtin_amdgcn_readfirstlane(n);   // segments before this one's turn
+                if (ahead <= 0) break;
+                if (ahead > 1) __builtin_amdgcn_s_sleep(1);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) h[i] = fmaf(p[i], in[i], h[i]);
-            *reinterpret_cast<f32x4 *>(slot_lds) = h;
+            *state = h;
             asm volatile("" ::: "memory");
-            if (lane == 0) done[nb] = seg + 1;   // LDS operations of a wave take effect in order
+            if (lane == 0) done[nb] = seg + 1;
+            __builtin_amdgcn_s_setprio(0);
             asm volatile("" ::: "memory");
-            if (live) {
-                if (slot >= 0)
-                    *reinterpret_cast<f32x4 *>(a.chunk_states + ((int64_t)slot * a.C_total + d) * N + nb * 16 + 4 * q) = h;
-                if (left <= SEG) *reinterpret_cast<f32x4 *>(a.final_states + state_row + nb * 16) = h;
+            if (slot >= 0) {
+                float *to = a.chunk_states + (int64_t)slot * a.C_total * N + nb * 16;   // uniform
+                if (live) *reinterpret_cast<f32x4 *>(to + state_col) = h;
+            }
+            if (!FULL || left == SEG) {
+                if (live) *reinterpret_cast<f32x4 *>(final + nb * 16 + state_col) = h;
             }
 
 #pragma unroll
@@ -305,9 +324,9 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) in[i] *= dec[t][i];
                 in = __builtin_amdgcn_mfma_f32_4x4x1f32(bt, du, in, 0, 0, 0);
-                float v = NBLK > 1 ? y[NBLK > 1 ? t : 0] : 0.0f;
+                float v = NBLK > 1 ? fmaf(in[0], cv[0], y[NBLK > 1 ? t : 0]) : in[0] * cv[0];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v = fmaf(in[i], cv[i], v);
+                for (int i = 1; i < 4; ++i) v = fmaf(in[i], cv[i], v);
                 y[NBLK > 1 ? t : t & 3] = v;
                 if constexpr (NBLK == 1) {
                     if (t % 4 == 3) emit(t / 4, {y[0], y[1], y[2], y[3]});
@@ -320,7 +339,11 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
 #pragma unroll
             for (int j = 0; j < J; ++j) emit(j, {y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]});
         }
-    }
+        py += nextY;
+    };
+    int seg = wave;
+    for (; (seg + 1) * SEG <= L; seg += nw) segment(seg, std::true_type{});
+    if (seg < nseg) segment(seg, std::false_type{});
 }
 
 // Waves of a scan workgroup

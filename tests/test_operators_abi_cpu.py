@@ -38,7 +38,7 @@ def _scan(m=None, **kw):
     (dict(N=8), UNSUPPORTED), (dict(N=48), UNSUPPORTED), (dict(N=512), UNSUPPORTED), (dict(u=None), NULL),
     (dict(dt=None), NULL), (dict(A=None), NULL), (dict(B=None), NULL), (dict(C=None), NULL), (dict(y=None), NULL),
     (dict(fin=None), NULL), (dict(us=63), SHAPE), (dict(ds=0), SHAPE), (dict(ys=-64), SHAPE), (dict(Bs=31), SHAPE),
-    (dict(Cs=16), SHAPE), (dict(zs=1), SHAPE), (dict(us=2 ** 28 + 1), SHAPE), (dict(u=FAKE + 1), SHAPE),
+    (dict(Cs=16), SHAPE), (dict(zs=1), SHAPE), (dict(us=2 ** 26 + 1), SHAPE), (dict(u=FAKE + 1), SHAPE),
     (dict(dtype=0, u=FAKE + 2), SHAPE), (dict(dtd=0, dt=FAKE + 2), SHAPE), (dict(A=FAKE + 4), SHAPE),
     (dict(init=FAKE + 8), SHAPE), (dict(fin=FAKE + 8), SHAPE), (dict(D=FAKE + 2), SHAPE), (dict(bias=FAKE + 1), SHAPE),
     (dict(cst=FAKE, cap=0), CAPACITY), (dict(cst=FAKE, cap=2), CAPACITY), (dict(cst=FAKE + 4, cap=9), SHAPE),
