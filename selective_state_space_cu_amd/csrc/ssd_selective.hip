@@ -87,6 +87,20 @@ template <> struct RawOf<float> {
     __device__ static f32x4 f4(const Four &v) { return f32x4{v.w[0], v.w[1], v.w[2], v.w[3]}; }
 };
 
+// One element at a uniform address plus a lane offset. The address is kept in scalar registers (the compiler would
+// add both per lane, in 64 bits) and the access stays a global one.
+template <typename V> using Global = __attribute__((address_space(1))) V;
+template <typename V> __device__ __forceinline__ V load_at(const char *base, uint32_t off) {
+    Global<const char> *p = (Global<const char> *)base;
+    asm("" : "+s"(p));
+    return *(Global<const V> *)(p + off);
+}
+template <typename V> __device__ __forceinline__ void store_at(char *base, uint32_t off, V v) {
+    Global<char> *p = (Global<char> *)base;
+    asm("" : "+s"(p));
+    *(Global<V> *)(p + off) = v;
+}
+
 // Sums of y_j (j < 4) over the four lanes 16 apart: lane (q, c) gets that of y_q.
 __device__ __forceinline__ float sum_scatter4(const float (&y)[4]) {
     auto swap32 = [](float a, float b) {   // [a.lo | b.lo] + [a.hi | b.hi]
@@ -134,8 +148,9 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q = lane >> 4, c = lane & 15, g = cb / bpg, ch = (cb - g * bpg) * kCh + c;
-    const bool live = ch < per;
-    const int d = g * per + (live ? ch : per - 1);
+    // Lanes past the group's channels are copies of its last channel: they compute and store the same values to the
+    // same places. (Stores without a branch keep the waits for the loads ahead of them exact.)
+    const int d = g * per + min(ch, per - 1);
 
     float *carry = lds;                                           // [NBLK][64][4]
     lds_counter *done = (lds_counter *)(__attribute__((address_space(3))) int *)(lds + NBLK * 256);   // [NBLK] segments finished
@@ -151,7 +166,7 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
     for (int nb = wave; nb < NBLK; nb += nw) {
         const f32x4 h = start ? *reinterpret_cast<const f32x4 *>(a.init + state_row + nb * 16 + state_col) : f32x4{0, 0, 0, 0};
         *reinterpret_cast<f32x4 *>(carry + (nb * 64 + lane) * 4) = h;
-        if (nseg == 0 && live) *reinterpret_cast<f32x4 *>(final + nb * 16 + state_col) = h;
+        if (nseg == 0) *reinterpret_cast<f32x4 *>(final + nb * 16 + state_col) = h;
         if (lane == 0) done[nb] = 0;
     }
     __syncthreads();
@@ -197,9 +212,9 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
     auto fetch = [&] {   // a segment of SEG tokens
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            ru[j] = *reinterpret_cast<const One *>(pu + 4 * j * su + offU);
-            rd[j] = *reinterpret_cast<const OneD *>(pd + 4 * j * sd + offD);
-            rz[j] = *reinterpret_cast<const One *>(pz + 4 * j * sz + offZ);
+            ru[j] = load_at<One>(pu + 4 * j * su, offU);
+            rd[j] = load_at<OneD>(pd + 4 * j * sd, offD);
+            rz[j] = load_at<One>(pz + 4 * j * sz, offZ);
         }
         fetch_bc(SEG, 0);
     };
@@ -245,7 +260,7 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
         auto emit = [&](int j, const float (&part)[4]) {   // tokens 4 j .. 4 j + 3
             float v = fmaf(skip, u[j], sum_scatter4(part));
             if (a.z != nullptr) v *= silu_full(R::f(z[j]));
-            if (live && (FULL || 4 * j + q < left)) *reinterpret_cast<T *>(py + 4 * j * sy + offY) = (T)v;
+            if (FULL || 4 * j + q < left) store_at<T>(py + 4 * j * sy, offY, (T)v);
         };
         float y[NBLK > 1 ? SEG : 4];
         if constexpr (NBLK > 1) {
@@ -310,10 +325,10 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
             asm volatile("" ::: "memory");
             if (slot >= 0) {
                 float *to = a.chunk_states + (int64_t)slot * a.C_total * N + nb * 16;   // uniform
-                if (live) *reinterpret_cast<f32x4 *>(to + state_col) = h;
+                *reinterpret_cast<f32x4 *>(to + state_col) = h;
             }
             if (!FULL || left == SEG) {
-                if (live) *reinterpret_cast<f32x4 *>(final + nb * 16 + state_col) = h;
+                *reinterpret_cast<f32x4 *>(final + nb * 16 + state_col) = h;
             }
 
 #pragma unroll
