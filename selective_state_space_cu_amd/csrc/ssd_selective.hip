@@ -285,19 +285,49 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
             }
             __builtin_amdgcn_wave_barrier();
 
+            // LDS values of the next tokens are on their way while these are computed (the compiler, left alone, either
+            // waits for each read or reads everything ahead and spills)
+            constexpr int G1 = 4, G2 = 2;   // tokens of a read group in the two passes
             f32x4 dec[SEG], h = {0, 0, 0, 0};
+            f32x2 dd[2][G1];
+            float bt[2][G1];
+            auto read1 = [&](int grp) {
 #pragma unroll
-            for (int t = 0; t < SEG; ++t) {
-                const f32x2 dd = *reinterpret_cast<const f32x2 *>(ldsD + (t * 16 + c) * 2);
-                const float bt = ldsB[t * 16 + 4 * q + (lane & 3)];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    dec[t][i] = fast_exp2(dd[0] * rate[i]);
-                    if (t > 0) h[i] *= dec[t][i];
+                for (int k = 0; k < G1; ++k) {
+                    const int t = grp * G1 + k;
+                    dd[grp & 1][k] = *reinterpret_cast<const f32x2 *>(ldsD + (t * 16 + c) * 2);
+                    bt[grp & 1][k] = ldsB[t * 16 + 4 * q + (lane & 3)];
                 }
-                h = __builtin_amdgcn_mfma_f32_4x4x1f32(bt, dd[1], h, 0, 0, 0);
-                if (t % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // bounds the LDS reads in flight, so the registers
+            };
+            read1(0);
+#pragma unroll
+            for (int grp = 0; grp < SEG / G1; ++grp) {
+                if (grp + 1 < SEG / G1) read1(grp + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int k = 0; k < G1; ++k) {
+                    const int t = grp * G1 + k;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        dec[t][i] = fast_exp2(dd[grp & 1][k][0] * rate[i]);
+                        if (t > 0) h[i] *= dec[t][i];
+                    }
+                    h = __builtin_amdgcn_mfma_f32_4x4x1f32(bt[grp & 1][k], dd[grp & 1][k][1], h, 0, 0, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
+            float du2[2][G2], bt2[2][G2];
+            f32x4 cv[2][G2];
+            auto read2 = [&](int grp) {
+#pragma unroll
+                for (int k = 0; k < G2; ++k) {
+                    const int t = grp * G2 + k;
+                    du2[grp & 1][k] = ldsD[(t * 16 + c) * 2 + 1];
+                    bt2[grp & 1][k] = ldsB[t * 16 + 4 * q + (lane & 3)];
+                    cv[grp & 1][k] = *reinterpret_cast<const f32x4 *>(ldsC + t * 16 + 4 * q);
+                }
+            };
+            read2(0);
             f32x4 p;
 #pragma unroll
             for (int i = 0; i < 4; ++i) p[i] = fast_exp2(sum * rate[i]);
@@ -332,21 +362,25 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
             }
 
 #pragma unroll
-            for (int t = 0; t < SEG; ++t) {
-                const float du = ldsD[(t * 16 + c) * 2 + 1];
-                const float bt = ldsB[t * 16 + 4 * q + (lane & 3)];
-                const f32x4 cv = *reinterpret_cast<const f32x4 *>(ldsC + t * 16 + 4 * q);
+            for (int grp = 0; grp < SEG / G2; ++grp) {
+                if (grp + 1 < SEG / G2) read2(grp + 1);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) in[i] *= dec[t][i];
-                in = __builtin_amdgcn_mfma_f32_4x4x1f32(bt, du, in, 0, 0, 0);
-                float v = NBLK > 1 ? fmaf(in[0], cv[0], y[NBLK > 1 ? t : 0]) : in[0] * cv[0];
+                for (int k = 0; k < G2; ++k) {
+                    const int t = grp * G2 + k;
+                    const f32x4 ct = cv[grp & 1][k];
 #pragma unroll
-                for (int i = 1; i < 4; ++i) v = fmaf(in[i], cv[i], v);
-                y[NBLK > 1 ? t : t & 3] = v;
-                if constexpr (NBLK == 1) {
-                    if (t % 4 == 3) emit(t / 4, {y[0], y[1], y[2], y[3]});
+                    for (int i = 0; i < 4; ++i) in[i] *= dec[t][i];
+                    in = __builtin_amdgcn_mfma_f32_4x4x1f32(bt2[grp & 1][k], du2[grp & 1][k], in, 0, 0, 0);
+                    float v = NBLK > 1 ? fmaf(in[0], ct[0], y[NBLK > 1 ? t : 0]) : in[0] * ct[0];
+#pragma unroll
+                    for (int i = 1; i < 4; ++i) v = fmaf(in[i], ct[i], v);
+                    y[NBLK > 1 ? t : t & 3] = v;
                 }
-                if (t % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                if constexpr (NBLK == 1) {
+                    if (grp & 1) emit(grp / 2, {y[0], y[1], y[2], y[3]});
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
             __builtin_amdgcn_wave_barrier();
         }
