@@ -152,6 +152,7 @@ struct SelectiveArgs {
     const int32_t *chunk_state_dst;     // slot per chunk or null (-> chunk index)
     const int32_t *cu_seqlens, *seq_chunk_start, *seq_order;
     int32_t cs, capacity, max_chunks;
+    int32_t walk_to;                    // sequences of at most this many tokens are walked by one wave (-1: none)
     // single tokens
     float *cache;                       // (num_slots, channels, N)
     const int32_t *read_slot, *write_slot;

@@ -12,9 +12,6 @@
 #include <type_traits>
 
 #include "ssd_scan.hpp"
-#ifndef SEL_SEG
-#define SEL_SEG 8
-#endif
 
 namespace ssd {
 
@@ -143,6 +140,7 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
     tb = tb < 0 ? 0 : (tb > a.T ? a.T : tb);
     te = te < tb ? tb : (te > a.T ? a.T : te);
     const int L = (int)(te - tb), c0 = a.seq_chunk_start[s];
+    if (L <= a.walk_to) return;   // the walk's
     const int nseg = (L + SEG - 1) / SEG, nw = (int)blockDim.x >> 6;
     const int chunk_segs = a.cs / SEG, chunk_shift = __builtin_ctz(chunk_segs);
 
@@ -395,8 +393,129 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
     if (seg < nseg) segment(seg, std::false_type{});
 }
 
-// Waves of a scan workgroup
-static int selective_waves(int64_t chains) { return chains >= 1024 ? 4 : chains >= 512 ? 8 : 16; }
+// ---------------------------------------------------------------------------
+// Scan, walked once: where there are sequences and channels enough to fill the
+// card, nothing runs side by side along a sequence, and the second pass and the
+// chain go. A wave owns 64 channels, lane = channel with all N states, and takes
+// token after token. B_t and C_t are the same for all lanes: they come through the
+// scalar cache into scalar registers, which the products take as operands (their
+// rows have to lie on 4-byte boundaries). Inputs are fetched K tokens ahead.
+template <typename T, typename DT, int N, int K>
+__global__ __launch_bounds__(64) void ssd_selective_walk_kernel(SelectiveArgs a) {
+    using R = RawOf<T>;
+    using RD = RawOf<DT>;
+    using One = typename R::One;
+    using OneD = typename RD::One;
+    constexpr int ES = sizeof(One), ED = sizeof(OneD), W = N * ES / 4;   // W: dwords of a row of B or C
+    typedef const __attribute__((address_space(4))) uint32_t scalar_words;
+    if (__builtin_nontemporal_load(a.error_flag) & SSD_DATA_BAD_CU_SEQLENS) return;
+    const int per = a.C_total / a.G, bpg = (per + 63) / 64, cblocks = a.G * bpg;
+    const int rank = blockIdx.x / cblocks, cb = blockIdx.x - rank * cblocks;
+    const int s = a.seq_order[rank];
+    if (s < 0 || s >= a.S) return;
+    int64_t tb = a.cu_seqlens[s], te = a.cu_seqlens[s + 1];
+    tb = tb < 0 ? 0 : (tb > a.T ? a.T : tb);
+    te = te < tb ? tb : (te > a.T ? a.T : te);
+    const int L = (int)(te - tb);
+    if (L > a.walk_to) return;   // the chain's
+    const int g = cb / bpg, lane = threadIdx.x;
+    const int d = g * per + min((cb - g * bpg) * 64 + lane, per - 1);   // (lanes past the end: copies of the last channel)
+    const int64_t state_row = (int64_t)s * a.C_total * N, state_col = (int64_t)d * N;
+    float h[N], rate[N];
+    const bool start = a.init != nullptr && (a.has_init == nullptr || a.has_init[s] != 0);
+#pragma unroll
+    for (int n = 0; n < N; n += 4) {
+        const f32x4 r = *reinterpret_cast<const f32x4 *>(a.A + state_col + n);
+        const f32x4 v = start ? *reinterpret_cast<const f32x4 *>(a.init + state_row + state_col + n) : f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            rate[n + i] = r[i] * kLog2e;
+            h[n + i] = v[i];
+        }
+    }
+    auto save = [&](float *to) {
+#pragma unroll
+        for (int n = 0; n < N; n += 4)
+            *reinterpret_cast<f32x4 *>(to + state_col + n) = f32x4{h[n], h[n + 1], h[n + 2], h[n + 3]};
+    };
+    const float bias = a.dt_bias != nullptr ? a.dt_bias[d] : 0.0f, skip = a.D != nullptr ? a.D[d] : 0.0f;
+    // uniform row pointers, advanced token by token (strides are below 2^28 bytes), plus 32-bit lane offsets
+    const uint32_t su = (uint32_t)a.u_stride * ES, sd = (uint32_t)a.dt_stride * ED, sy = (uint32_t)a.y_stride * ES,
+                   sz = (uint32_t)(a.z ? a.z_stride : a.u_stride) * ES, sB = (uint32_t)a.B_stride * ES,
+                   sC = (uint32_t)a.C_stride * ES;
+    const char *pu = reinterpret_cast<const char *>(a.u) + tb * su, *pd = reinterpret_cast<const char *>(a.dt) + tb * sd;
+    const char *pz = reinterpret_cast<const char *>(a.z ? a.z : a.u) + tb * sz;   // (no gate: u again, unused)
+    char *py = reinterpret_cast<char *>(a.y) + tb * sy;
+    const char *pB = reinterpret_cast<const char *>(a.B) + tb * sB + g * N * ES;
+    const char *pC = reinterpret_cast<const char *>(a.C) + tb * sC + g * N * ES;
+    const uint32_t offT = d * ES, offD = d * ED;
+
+    One ru[K], rz[K];
+    OneD rd[K];
+    int ahead = 0;   // the token that the next fetch reads (past the end: the last one again)
+    auto fetch = [&](int k) {
+        ru[k] = load_at<One>(pu, offT);
+        rd[k] = load_at<OneD>(pd, offD);
+        rz[k] = load_at<One>(pz, offT);
+        const bool more = ++ahead < L;
+        pu += more ? su : 0;
+        pd += more ? sd : 0;
+        pz += more ? sz : 0;
+    };
+    auto value = [](const uint32_t (&w)[W], int n) -> float {
+        if constexpr (ES == 4) return __uint_as_float(w[n]);
+        else return __uint_as_float(n & 1 ? w[n / 2] & 0xffff0000u : w[n / 2] << 16);
+    };
+    auto token = [&](int k) {
+        uint32_t wB[W], wC[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) wB[i] = ((scalar_words *)pB)[i];
+#pragma unroll
+        for (int i = 0; i < W; ++i) wC[i] = ((scalar_words *)pC)[i];
+        const float u = R::f(ru[k]), delta = softplus_full(RD::f(rd[k]) + bias), du = delta * u;
+        const One z = rz[k];
+        fetch(k);
+        float y[2] = {skip * u, 0.0f};
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            h[n] = fmaf(fast_exp2(delta * rate[n]), h[n], du * value(wB, n));
+            y[n & 1] = fmaf(h[n], value(wC, n), y[n & 1]);
+        }
+        float v = y[0] + y[1];
+        if (a.z != nullptr) v *= silu_full(R::f(z));
+        store_at<T>(py, offT, (T)v);
+        pB += sB;
+        pC += sC;
+        py += sy;
+    };
+    if (L > 0) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) fetch(k);
+    }
+    // chunks of the batch's grid, in runs of K tokens (K divides the chunk size)
+    const int step = a.chunk_states != nullptr ? a.cs : L;
+    int chunk = a.seq_chunk_start[s];
+    for (int t0 = 0; t0 < L; t0 += step, ++chunk) {
+        const int end = min(t0 + step, L);
+        int t = t0;
+        for (; t + K <= end; t += K) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) token(k);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)   // the sequence's last tokens
+            if (t + k < end) token(k);
+        if (a.chunk_states != nullptr) {
+            const int slot = a.chunk_state_dst != nullptr ? a.chunk_state_dst[chunk] : chunk;
+            if (slot >= a.capacity) {
+                if (cb == 0 && lane == 0) atomicOr(a.error_flag, SSD_DATA_BAD_SLOT);
+            } else if (slot >= 0) {
+                save(a.chunk_states + (int64_t)slot * a.C_total * N);
+            }
+        }
+    }
+    save(a.final_states + state_row);
+}
 
 // Step: lanes own 4 consecutive states of one channel (N / 4 lanes a channel).
 constexpr int kSelStepThreads = 256;
@@ -439,16 +558,52 @@ __global__ __launch_bounds__(kSelStepThreads) void ssd_selective_step_kernel(Sel
     }
 }
 
+// Waves of a workgroup that splits sequences into segments: the fewer (sequence,
+// 16 channels) pairs there are, the more. 2560 pairs (8 ragged prompts): 4 waves
+// 374 us, 8 waves 388, 16 waves 476; 1024 pairs (4 x 8894 tokens): 745, 730, 793;
+// 160 pairs (one prompt of 30001 tokens): 1071, 718, 649.
+static int segment_waves(int64_t pairs) { return pairs >= 1024 ? 4 : pairs >= 512 ? 8 : 16; }
+
+// From this many (sequence, 64 channels) pairs on, 4 for every SIMD, sequences
+// are walked (64 prompts of 1 to 490 tokens, 8192 channels: 690 us in segments,
+// 460 walked; 8 prompts of 5120 channels, 640 pairs: 390 and 2150).
+constexpr int64_t kWalkPairs = 4096;
+// A walk takes as long as its sequence, so one much longer than the others would
+// be left over: those of more than 3 times the mean length go in segments.
+constexpr int64_t kWalkTimesMean = 3;
+
 template <typename T, typename DT, int N> struct SelectiveLaunch {
-    static hipError_t scan(const SelectiveArgs &a, hipStream_t stream) {
-        const int64_t blocks = (int64_t)a.S * a.G * ((a.C_total / a.G + kCh - 1) / kCh);
-        const int waves = selective_waves(blocks);
+    static constexpr int SEG = 8;   // tokens of a segment (16: 128 registers do not hold the decays, 872 us against 771)
+    // Sequences of more than a.walk_to tokens, among the `ranks` longest, in segments.
+    static hipError_t segments(const SelectiveArgs &a, int64_t ranks, hipStream_t stream) {
+        const int64_t blocks = ranks * a.G * ((a.C_total / a.G + kCh - 1) / kCh);
+        const int waves = segment_waves(blocks);
         constexpr int NBLK = N / 16;
-        constexpr int SEG = SEL_SEG;
         const size_t lds = sizeof(float) * (NBLK * 256 + ((NBLK + 3) & ~3) + (size_t)waves * SEG * 64);
-        hipLaunchKernelGGL((ssd_selective_scan_kernel<T, DT, N, SEG>), dim3((unsigned)blocks), dim3(64 * waves), lds, stream,
-                           a);
+        hipLaunchKernelGGL((ssd_selective_scan_kernel<T, DT, N, SEG>), dim3((unsigned)blocks), dim3(64 * waves), lds,
+                           stream, a);
         return hipGetLastError();
+    }
+    static hipError_t scan(SelectiveArgs a, hipStream_t stream) {
+        a.walk_to = -1;
+        if constexpr (N <= 32) {
+            const int64_t walks = (int64_t)a.S * a.G * ((a.C_total / a.G + 63) / 64);
+            const bool scalar_rows = sizeof(T) == 4 || ((a.B_stride | a.C_stride) % 2 == 0 &&
+                (reinterpret_cast<uintptr_t>(a.B) | reinterpret_cast<uintptr_t>(a.C)) % 4 == 0);
+            if (scalar_rows && walks >= kWalkPairs) {
+                const int64_t limit = kWalkTimesMean * ((a.T + (int64_t)a.S - 1) / a.S);
+                a.walk_to = (int32_t)(limit < a.T ? limit : a.T);
+                const int64_t ranks = a.T / (a.walk_to + 1);   // no more sequences are that long
+                if (ranks > 0) {
+                    const hipError_t e = segments(a, ranks, stream);
+                    if (e != hipSuccess) return e;
+                }
+                hipLaunchKernelGGL((ssd_selective_walk_kernel<T, DT, N, 2>), dim3((unsigned)walks), dim3(64), 0, stream,
+                                   a);
+                return hipGetLastError();
+            }
+        }
+        return segments(a, a.S, stream);
     }
     static hipError_t step(const SelectiveArgs &a, hipStream_t stream) {
         const int64_t items = (int64_t)a.S * a.C_total * (N / 4);

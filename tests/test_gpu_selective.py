@@ -375,3 +375,80 @@ def test_two_streams_at_once():
     for k, g in enumerate(got):
         want = (wi, wj)[k % 2]
         assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1])
+
+
+def many(lengths, d, n, g, dtype, seed, pad=0, chunk=64, **kw):
+    """Enough (sequence, channels) pairs that sequences are walked one wave each, and a few far longer ones that
+    are not; every channel of a few sequences against float64, others in the batch and alone."""
+    i = make(lengths, d, n, g, dtype, seed=seed, **kw)
+    if pad == 0:   # rows of B and C on 4-byte boundaries
+        wide = torch.cat([i["B"].reshape(-1, g * n), i["C"].reshape(-1, g * n)], 1).contiguous()
+        i["B"], i["C"] = wide[:, :g * n].unflatten(1, (g, n)), wide[:, g * n:].unflatten(1, (g, n))
+    meta = ssd.varlen_metadata(i["cu"], chunk, total_tokens=sum(lengths))
+    cst = torch.full((meta.max_chunks, d, n), float("nan"), device="cuda")
+    y, fin, meta = call(i, chunk=chunk, chunk_states=cst)
+    assert int(meta.error_flag.item()) == 0
+    assert torch.isfinite(fin).all()
+    return i, y, fin, cst
+
+
+def sequence(i, s):
+    """One sequence of a batch as a batch of its own."""
+    t0 = sum(i["lengths"][:s])
+    r = slice(t0, t0 + i["lengths"][s])
+    j = {**i, "lengths": [i["lengths"][s]], "cu": torch.tensor([0, i["lengths"][s]], dtype=torch.int32, device="cuda")}
+    for k in ("u", "dt", "B", "C", "z"):
+        j[k] = None if i[k] is None else i[k][r]
+    j["init"] = None if i["init"] is None else i["init"][s:s + 1].contiguous()
+    j["has"] = None if i["has"] is None else i["has"][s:s + 1]
+    return j, r
+
+
+@pytest.mark.parametrize("dtype,n,g,gate,init", [
+    (BF, 16, 1, True, "even"), (BF, 32, 2, False, "all"), (F32, 16, 2, True, "none"), (F32, 32, 1, True, "even"),
+])
+def test_scan_of_many_sequences(dtype, n, g, gate, init):
+    """512 sequences of 8 x 64 + 2 x 5 channels: 4608 or more pairs."""
+    lengths = [int(v) for v in torch.randint(0, 40, (512,), generator=torch.Generator().manual_seed(n + g))]
+    lengths[3], lengths[77], lengths[200], lengths[201] = 700, 333, 0, 1
+    d = 522
+    i, y, fin, cst = many(lengths, d, n, g, dtype, seed=30 + n, gate=gate, init=init)
+    first = 0
+    starts_of = []
+    for v in lengths:
+        starts_of.append(first)
+        first += -(-v // 64)
+    for s in (0, 1, 3, 77, 200, 201, 511):
+        j, r = sequence(i, s)
+        ry, rh, by, bh, start = expected(j)[0]
+        ref.check(y[r], ry, by, f"y of {s}")
+        if lengths[s] == 0:
+            want = torch.zeros(d, n) if start is None else start
+            assert torch.equal(fin[s].cpu(), want)
+            continue
+        ref.check(fin[s], rh[-1], bh[-1], f"state of {s}")
+        for k in range(-(-lengths[s] // 64)):
+            last = min(64 * k + 64, lengths[s]) - 1
+            ref.check(cst[starts_of[s] + k], rh[last], bh[last], f"chunk {k} of {s}")
+    assert torch.isnan(cst[first:]).all()
+    for s in range(5, 512, 50):
+        # One alone goes in segments. Sums in another order differ by float32's roundings before y's own: each result
+        # is within the reference's bound (which counts those) plus one rounding of y, so each is checked against it.
+        j, r = sequence(i, s)
+        if lengths[s] == 0:
+            continue
+        y1, f1, _ = call(j)
+        ry, rh, by, bh, _ = expected(j)[0]
+        for name, gy, gf in (("batch", y[r], fin[s]), ("alone", y1, f1[0])):
+            ref.check(gy, ry, by, f"y of {s} ({name})")
+            ref.check(gf, rh[-1], bh[-1], f"state of {s} ({name})")
+
+
+def test_scan_of_many_sequences_with_odd_rows():
+    """Rows of B and C that do not lie on 4-byte boundaries go in segments; so does any number of sequences."""
+    lengths = [7] * 300
+    i, y, fin, _ = many(lengths, 1030, 16, 1, BF, seed=44, pad=1)
+    j, r = sequence(i, 150)
+    ry, rh, by, bh, _ = expected(j)[0]
+    ref.check(y[r], ry, by, "y")
+    ref.check(fin[150], rh[-1], bh[-1], "state")
