@@ -235,61 +235,97 @@ hipError_t launch_conv1d(const Conv1dArgs &a, bool bf16, hipStream_t stream) {
 }
 
 // One new token per sequence: the same convolution, its window read from one
-// slot and written, shifted by the token, to another. Memory-bound and small:
-// each lane owns 8 channels of one sequence.
-template <typename T, int W>
+// slot and written, shifted by the token, to another. Memory-bound: each lane
+// owns 8 channels and takes SEQS sequences, one after the other, whose loads are
+// on their way together and share the lane's taps (a sequence's windows are 8
+// bytes a channel in bf16, the taps 16).
+template <typename T, int W, int SEQS>
 __global__ __launch_bounds__(kConvThreads) void ssd_conv1d_step_kernel(Conv1dStepArgs a) {
     constexpr int WR = W > 1 ? W - 1 : 1;   // window rows (at least one, unused when W = 1)
     using IO = ConvIO<T>;
     const int per = kConvThreads * kConvVec, nxb = (a.C + per - 1) / per;
-    const int s = blockIdx.x / nxb;
-    const int ch = ((blockIdx.x - s * nxb) * kConvThreads + threadIdx.x) * kConvVec;
+    const int sg = blockIdx.x / nxb;
+    const int ch = ((blockIdx.x - sg * nxb) * kConvThreads + threadIdx.x) * kConvVec;
     if (ch >= a.C) return;
-    const int rs = a.read_slot != nullptr ? a.read_slot[s] : -1;
-    const int ws = a.write_slot != nullptr ? a.write_slot[s] : -1;
-    if (rs >= a.num_slots || ws >= a.num_slots) {   // refused: nothing read or written
-        if (ch == 0 && a.error_flag != nullptr) atomicOr(a.error_flag, SSD_DATA_BAD_SLOT);
-        return;
-    }
     const int64_t C = a.C, slot_elems = (int64_t)(W - 1) * C;
-    float win[WR][kConvVec], xv[kConvVec], o[kConvVec];
-    IO::load(a.x, (int64_t)s * a.x_stride + ch, xv);
+    typename IO::Raw win[SEQS][WR], xr[SEQS];
+    int rs[SEQS], ws[SEQS];
+    bool taken[SEQS];
 #pragma unroll
-    for (int i = 0; i < W - 1; ++i) {
-        if (rs >= 0) IO::load(a.states, rs * slot_elems + i * C + ch, win[i]);
-        else {
-#pragma unroll
-            for (int v = 0; v < kConvVec; ++v) win[i][v] = 0.0f;
+    for (int k = 0; k < SEQS; ++k) {
+        const int s = sg * SEQS + k;
+        taken[k] = s < a.S;
+        if (!taken[k]) continue;
+        rs[k] = a.read_slot != nullptr ? a.read_slot[s] : -1;
+        ws[k] = a.write_slot != nullptr ? a.write_slot[s] : -1;
+        if (rs[k] >= a.num_slots || ws[k] >= a.num_slots) {   // refused: nothing read or written
+            if (ch == 0 && a.error_flag != nullptr) atomicOr(a.error_flag, SSD_DATA_BAD_SLOT);
+            taken[k] = false;
+            continue;
         }
+        xr[k] = IO::raw(a.x, (int64_t)s * a.x_stride + ch);
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i)
+            win[k][i] = rs[k] >= 0 ? IO::raw(a.states, rs[k] * slot_elems + i * C + ch) : typename IO::Raw{};
     }
+    float w[W][kConvVec], bias[kConvVec];
 #pragma unroll
     for (int v = 0; v < kConvVec; ++v) {
-        const float *w = a.weight + (int64_t)(ch + v) * W;
-        float z = a.bias != nullptr ? a.bias[ch + v] : 0.0f;
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) z = fmaf(w[k], win[k][v], z);
-        z = fmaf(w[W - 1], xv[v], z);
-        o[v] = a.silu ? silu(z) : z;
+        for (int k = 0; k < W; ++k) w[k][v] = a.weight[(int64_t)(ch + v) * W + k];
+        bias[v] = a.bias != nullptr ? a.bias[ch + v] : 0.0f;
     }
-    IO::store(a.out, (int64_t)s * a.out_stride + ch, o, false);
-    if (ws >= 0) {
 #pragma unroll
-        for (int i = 0; i + 1 < W - 1; ++i) IO::store(a.states, ws * slot_elems + i * C + ch, win[i + 1], false);
-        if constexpr (W > 1) IO::store(a.states, ws * slot_elems + (W - 2) * C + ch, xv, false);
+    for (int k = 0; k < SEQS; ++k) {
+        if (!taken[k]) continue;
+        const int s = sg * SEQS + k;
+        float o[kConvVec], u[W][kConvVec];
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) IO::unpack(win[k][i], u[i]);
+        IO::unpack(xr[k], u[W - 1]);
+#pragma unroll
+        for (int v = 0; v < kConvVec; ++v) {
+            float z = bias[v];
+#pragma unroll
+            for (int i = 0; i < W; ++i) z = fmaf(w[i][v], u[i][v], z);
+            o[v] = a.silu ? silu(z) : z;
+        }
+        IO::store(a.out, (int64_t)s * a.out_stride + ch, o, false);
+        if (ws[k] >= 0) {
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) IO::store(a.states, ws[k] * slot_elems + i * C + ch, u[i + 1], false);
+        }
     }
+}
+
+// A step takes this many sequences to a workgroup where that still makes 2 workgroups for every CU (256 sequences of
+// 10240 bf16 channels, width 4: 1 / 2 / 4 / 8 sequences 19.0 / 14.2 / 12.5 / 14.7 us; 42 MB, so 3.4 TB/s, of which the
+// launch is about 3 us).
+constexpr int kConvStepSeqs = 4;
+constexpr int64_t kConvStepFill = 512;
+
+template <typename T, int W>
+static hipError_t launch_conv1d_step_w(const Conv1dStepArgs &a, hipStream_t stream) {
+    const int64_t nxb = conv1d_channel_blocks(a.C), groups = ((int64_t)a.S + kConvStepSeqs - 1) / kConvStepSeqs;
+    const dim3 block(kConvThreads);
+    if (!fits_grid(a.S * nxb, kConvThreads)) return hipErrorInvalidConfiguration;
+    if (groups * nxb >= kConvStepFill)
+        hipLaunchKernelGGL((ssd_conv1d_step_kernel<T, W, kConvStepSeqs>), dim3((unsigned)(groups * nxb)), block, 0,
+                           stream, a);
+    else
+        hipLaunchKernelGGL((ssd_conv1d_step_kernel<T, W, 1>), dim3((unsigned)(a.S * nxb)), block, 0, stream, a);
+    return hipGetLastError();
 }
 
 template <typename T>
 static hipError_t launch_conv1d_step_t(const Conv1dStepArgs &a, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)a.S * conv1d_channel_blocks(a.C))), block(kConvThreads);
     switch (a.W) {
-        case 1: hipLaunchKernelGGL((ssd_conv1d_step_kernel<T, 1>), grid, block, 0, stream, a); break;
-        case 2: hipLaunchKernelGGL((ssd_conv1d_step_kernel<T, 2>), grid, block, 0, stream, a); break;
-        case 3: hipLaunchKernelGGL((ssd_conv1d_step_kernel<T, 3>), grid, block, 0, stream, a); break;
-        case 4: hipLaunchKernelGGL((ssd_conv1d_step_kernel<T, 4>), grid, block, 0, stream, a); break;
+        case 1: return launch_conv1d_step_w<T, 1>(a, stream);
+        case 2: return launch_conv1d_step_w<T, 2>(a, stream);
+        case 3: return launch_conv1d_step_w<T, 3>(a, stream);
+        case 4: return launch_conv1d_step_w<T, 4>(a, stream);
         default: return hipErrorInvalidValue;
     }
-    return hipGetLastError();
 }
 
 hipError_t launch_conv1d_step(const Conv1dStepArgs &a, bool bf16, hipStream_t stream) {

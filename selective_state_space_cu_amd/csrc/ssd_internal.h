@@ -136,6 +136,9 @@ constexpr size_t kGdnScratchBytes = size_t(32) << 20;
 constexpr int kMaxDevices = 64;
 hipError_t gdn_scratch(void **ptr);
 
+// Whether a one-dimensional launch is within the runtime's limit of 2^32 - 1 threads.
+inline bool fits_grid(int64_t blocks, int64_t threads) { return blocks <= INT64_C(0xffffffff) / threads; }
+
 // Selective scan with a decay per channel and state (see ssd_selective.hip):
 // prompts (tokens of packed sequences) and single tokens (one row each).
 struct SelectiveArgs {

@@ -517,41 +517,64 @@ __global__ __launch_bounds__(64) void ssd_selective_walk_kernel(SelectiveArgs a)
     save(a.final_states + state_row);
 }
 
-// Step: lanes own 4 consecutive states of one channel (N / 4 lanes a channel).
+// ---------------------------------------------------------------------------
+// Step. Memory-bound: the state slots are the traffic (8 N bytes a sequence and
+// channel). Lanes own 4 consecutive states of one channel (N / 4 lanes a
+// channel), so a workgroup moves whole contiguous runs; it takes SEQS sequences
+// at once, whose slots and states are then on their way together and share the
+// rates A.
 constexpr int kSelStepThreads = 256;
 
-template <typename T, typename DT, int N>
-__global__ __launch_bounds__(kSelStepThreads) void ssd_selective_step_kernel(SelectiveArgs a, int64_t items) {
-    constexpr int LPC = N / 4;   // lanes of a channel
-    for (int64_t id = (int64_t)blockIdx.x * kSelStepThreads + threadIdx.x; id < items;
-         id += (int64_t)gridDim.x * kSelStepThreads) {
-        const int64_t sc = id / LPC;
-        const int nq = (int)(id - sc * LPC);
-        const int s = (int)(sc / a.C_total), d = (int)(sc - (int64_t)s * a.C_total);
-        const int rs = a.read_slot[s], ws = a.write_slot[s];
-        if (rs >= a.num_slots || ws >= a.num_slots) {   // refused: nothing read or written
+template <typename T, typename DT, int N, int SEQS>
+__global__ __launch_bounds__(kSelStepThreads) void ssd_selective_step_kernel(SelectiveArgs a) {
+    constexpr int LPC = N / 4, CH = kSelStepThreads / LPC;   // lanes of a channel, channels of a workgroup
+    using R = RawOf<T>;
+    const int cblocks = (a.C_total + CH - 1) / CH;
+    const int sg = blockIdx.x / cblocks, cb = blockIdx.x - sg * cblocks;
+    const int nq = threadIdx.x % LPC, d = cb * CH + (int)threadIdx.x / LPC;
+    if (d >= a.C_total) return;   // whole channels, so whole shuffle groups, leave together
+    const int n0 = d / (a.C_total / a.G) * N + 4 * nq;
+    const int64_t slot = (int64_t)a.C_total * N, at = (int64_t)d * N + 4 * nq;
+    int ws[SEQS];
+    bool taken[SEQS];
+    f32x4 h[SEQS];
+    // states first (the traffic), then the small operands
+#pragma unroll
+    for (int k = 0; k < SEQS; ++k) {
+        const int s = sg * SEQS + k;
+        h[k] = f32x4{0, 0, 0, 0};
+        taken[k] = s < a.S;
+        if (!taken[k]) continue;
+        const int rs = a.read_slot[s];
+        ws[k] = a.write_slot[s];
+        if (rs >= a.num_slots || ws[k] >= a.num_slots) {   // refused: nothing read or written
             if (d == 0 && nq == 0 && a.error_flag != nullptr) atomicOr(a.error_flag, SSD_DATA_BAD_SLOT);
-            continue;   // whole channels, so whole shuffle groups, leave together
+            taken[k] = false;
+            continue;
         }
-        const int g = d / (a.C_total / a.G);
-        const int64_t slot = (int64_t)a.C_total * N, at = (int64_t)d * N + 4 * nq;
-        f32x4 h = rs >= 0 ? *reinterpret_cast<const f32x4 *>(a.cache + rs * slot + at) : f32x4{0, 0, 0, 0};
-        const f32x4 rate = *reinterpret_cast<const f32x4 *>(a.A + at);
+        if (rs >= 0) h[k] = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(a.cache + rs * slot + at));
+    }
+    const f32x4 rate = *reinterpret_cast<const f32x4 *>(a.A + at) * kLog2e;
+    const float bias = a.dt_bias != nullptr ? a.dt_bias[d] : 0.0f, skip = a.D != nullptr ? a.D[d] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < SEQS; ++k) {
+        if (!taken[k]) continue;
+        const int64_t s = sg * SEQS + k;
         const float u = load_f<T>(a.u, s * a.u_stride + d);
-        const float delta = softplus_full(load_f<DT>(a.dt, s * a.dt_stride + d) + (a.dt_bias ? a.dt_bias[d] : 0.0f));
+        const float delta = softplus_full(load_f<DT>(a.dt, s * a.dt_stride + d) + bias), du = delta * u;
+        const f32x4 bv = R::f4(*reinterpret_cast<const typename R::Four *>(reinterpret_cast<const T *>(a.B) + s * a.B_stride + n0));
+        const f32x4 cv = R::f4(*reinterpret_cast<const typename R::Four *>(reinterpret_cast<const T *>(a.C) + s * a.C_stride + n0));
         float y = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int n = g * N + 4 * nq + i;
-            h[i] = fmaf(fast_exp2(delta * (rate[i] * kLog2e)), h[i],
-                        delta * u * load_f<T>(a.B, s * a.B_stride + n));
-            y = fmaf(h[i], load_f<T>(a.C, s * a.C_stride + n), y);
+            h[k][i] = fmaf(fast_exp2(delta * rate[i]), h[k][i], du * bv[i]);
+            y = fmaf(h[k][i], cv[i], y);
         }
-        if (ws >= 0) *reinterpret_cast<f32x4 *>(a.cache + ws * slot + at) = h;
+        if (ws[k] >= 0) __builtin_nontemporal_store(h[k], reinterpret_cast<f32x4 *>(a.cache + ws[k] * slot + at));
 #pragma unroll
         for (int m = LPC / 2; m >= 1; m >>= 1) y += __shfl_xor(y, m, LPC);
         if (nq == 0) {
-            y = fmaf(a.D != nullptr ? a.D[d] : 0.0f, u, y);
+            y = fmaf(skip, u, y);
             if (a.z != nullptr) y *= silu_full(load_f<T>(a.z, s * a.z_stride + d));
             reinterpret_cast<T *>(a.y)[s * a.y_stride + d] = (T)y;
         }
@@ -572,12 +595,18 @@ constexpr int64_t kWalkPairs = 4096;
 // be left over: those of more than 3 times the mean length go in segments.
 constexpr int64_t kWalkTimesMean = 3;
 
+// A step takes this many sequences to a workgroup where that still makes 8 workgroups for every CU (256 sequences of
+// 5120 channels, 16 states: 1 / 2 / 4 / 8 sequences 41.8 / 39.7 / 40.9 / 98 us; 179 MB, so 4.5 TB/s).
+constexpr int kStepSeqs = 2;
+constexpr int64_t kStepFill = 2048;
+
 template <typename T, typename DT, int N> struct SelectiveLaunch {
     static constexpr int SEG = 8;   // tokens of a segment (16: 128 registers do not hold the decays, 872 us against 771)
     // Sequences of more than a.walk_to tokens, among the `ranks` longest, in segments.
     static hipError_t segments(const SelectiveArgs &a, int64_t ranks, hipStream_t stream) {
         const int64_t blocks = ranks * a.G * ((a.C_total / a.G + kCh - 1) / kCh);
         const int waves = segment_waves(blocks);
+        if (!fits_grid(blocks, 64 * waves)) return hipErrorInvalidConfiguration;
         constexpr int NBLK = N / 16;
         const size_t lds = sizeof(float) * (NBLK * 256 + ((NBLK + 3) & ~3) + (size_t)waves * SEG * 64);
         hipLaunchKernelGGL((ssd_selective_scan_kernel<T, DT, N, SEG>), dim3((unsigned)blocks), dim3(64 * waves), lds,
@@ -591,6 +620,7 @@ template <typename T, typename DT, int N> struct SelectiveLaunch {
             const bool scalar_rows = sizeof(T) == 4 || ((a.B_stride | a.C_stride) % 2 == 0 &&
                 (reinterpret_cast<uintptr_t>(a.B) | reinterpret_cast<uintptr_t>(a.C)) % 4 == 0);
             if (scalar_rows && walks >= kWalkPairs) {
+                if (!fits_grid(walks, 64)) return hipErrorInvalidConfiguration;
                 const int64_t limit = kWalkTimesMean * ((a.T + (int64_t)a.S - 1) / a.S);
                 a.walk_to = (int32_t)(limit < a.T ? limit : a.T);
                 const int64_t ranks = a.T / (a.walk_to + 1);   // no more sequences are that long
@@ -605,13 +635,18 @@ template <typename T, typename DT, int N> struct SelectiveLaunch {
         }
         return segments(a, a.S, stream);
     }
-    static hipError_t step(const SelectiveArgs &a, hipStream_t stream) {
-        const int64_t items = (int64_t)a.S * a.C_total * (N / 4);
-        const int64_t want = (items + kSelStepThreads - 1) / kSelStepThreads;
-        const unsigned blocks = (unsigned)(want < (1 << 20) ? want : (1 << 20));
-        hipLaunchKernelGGL((ssd_selective_step_kernel<T, DT, N>), dim3(blocks), dim3(kSelStepThreads), 0, stream, a,
-                           items);
+    template <int SEQS> static hipError_t steps(const SelectiveArgs &a, int64_t blocks, hipStream_t stream) {
+        if (!fits_grid(blocks, kSelStepThreads)) return hipErrorInvalidConfiguration;
+        hipLaunchKernelGGL((ssd_selective_step_kernel<T, DT, N, SEQS>), dim3((unsigned)blocks), dim3(kSelStepThreads), 0,
+                           stream, a);
         return hipGetLastError();
+    }
+    static hipError_t step(const SelectiveArgs &a, hipStream_t stream) {
+        constexpr int CH = kSelStepThreads / (N / 4);
+        const int64_t cblocks = (a.C_total + CH - 1) / CH;
+        const int64_t groups = ((int64_t)a.S + kStepSeqs - 1) / kStepSeqs;
+        if (groups * cblocks >= kStepFill) return steps<kStepSeqs>(a, groups * cblocks, stream);
+        return steps<1>(a, a.S * cblocks, stream);
     }
 };
 

@@ -471,50 +471,57 @@ def _enqueue(fn, device, *args):
     """Call the library's `fn` on the current stream of `device`, with that device current."""
     if device.type != "cuda":
         raise ValueError(f"{fn} needs tensors on a GPU, got {device}")
-    f = getattr(load_library(), fn)
+    f = getattr(_lib or load_library(), fn)
     if device.index == torch.cuda.current_device():
-        status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+        status = f(*args, torch._C._cuda_getCurrentRawStream(device.index))
     else:
         with torch.cuda.device(device):
-            status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+            status = f(*args, torch._C._cuda_getCurrentRawStream(device.index))
     if status != 0:
         raise SSDError(fn, status, status_string(status))
 
 
-def _address(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _rows(t: torch.Tensor, name: str, device, dtype, shape) -> int:
-    """A tensor of `shape` (rows first) whose rows are contiguous but may lie any distance apart, as a slice of
-    a wider projection has them. Returns the elements from one row to the next."""
+def _refuse(t: torch.Tensor, name: str, device, dtype, shape):
+    """Says what is wrong with a tensor that is not as it has to be."""
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    row = 1
+    raise ValueError(f"{name} must be contiguous, or where rows may lie apart have contiguous rows; got strides "
+                     f"{t.stride()}")
+
+
+def _whole(t: Optional[torch.Tensor], name: str, device, dtype, shape):
+    """Checks a contiguous tensor; returns its address (None for None)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        _refuse(t, name, device, dtype, shape)
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, device, dtype, shape, row: int) -> int:
+    """Checks a tensor of `shape` (rows first, `row` elements each) whose rows are contiguous but may lie any distance
+    apart, as a slice of a wider projection has them. Returns the elements from one row to the next."""
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _refuse(t, name, device, dtype, shape)
+    if t.is_contiguous():
+        return row
+    step = 1
     for size, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != row:
-            raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
-        row *= size
+        if size != 1 and stride != step:
+            _refuse(t, name, device, dtype, shape)
+        step *= size
     return t.stride(0) if shape[0] > 1 else row
 
 
-def _params(device, **named):
-    """float32 parameters and states: (tensor or None, shape) by name."""
-    for name, (t, shape) in named.items():
-        if t is not None:
-            _shape(t, name, *shape)
-            _data(t, name, device, torch.float32)
-
-
-def _out_rows(out: Optional[torch.Tensor], name: str, like: torch.Tensor):
+def _out_rows(out: Optional[torch.Tensor], name: str, like: torch.Tensor, row: int):
     """The output and the elements between its rows: `out` if given, else a new contiguous one."""
     if out is None:
-        out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    return out, _rows(out, name, like.device, like.dtype, like.shape)
+        return torch.empty_like(like, memory_format=torch.contiguous_format), row
+    return out, _rows(out, name, like.device, like.dtype, like.shape, row)
 
 
 def _selective_inputs(u, dt, A, B, C, dt_bias, D, z):
@@ -522,20 +529,32 @@ def _selective_inputs(u, dt, A, B, C, dt_bias, D, z):
     if u.dim() != 2 or B.dim() != 3:
         raise ValueError(f"u must be (rows, channels) and B (rows, groups, states), got {tuple(u.shape)} and "
                          f"{tuple(B.shape)}")
-    device, dtype = u.device, u.dtype
-    if dt.dtype not in (torch.float32, torch.bfloat16):
+    device, dtype, shape, bshape = u.device, u.dtype, u.shape, B.shape
+    rows, channels = shape
+    brows, groups, n = bshape
+    code = _dtype_code(u)
+    if dt.dtype != dtype and dt.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"dt must be float32 or bfloat16, got {dt.dtype}")
-    rows, channels = u.shape
-    groups, n = B.shape[1], B.shape[2]
-    strides = [_rows(u, "u", device, dtype, u.shape), _rows(dt, "dt", device, dt.dtype, u.shape),
-               _rows(B, "B", device, dtype, B.shape), _rows(C, "C", device, dtype, B.shape),
-               0 if z is None else _rows(z, "z", device, dtype, u.shape)]
-    if B.shape[0] != rows:
-        raise ValueError(f"B must have {rows} rows, got {B.shape[0]}")
-    _params(device, A=(A, (channels, n)), dt_bias=(dt_bias, (channels,)), D=(D, (channels,)))
-    return (u.data_ptr(), strides[0], dt.data_ptr(), strides[1], _address(dt_bias), A.data_ptr(), B.data_ptr(),
-            strides[2], C.data_ptr(), strides[3], _address(D), _address(z), strides[4], _dtype_code(u),
-            _dtype_code(dt)), channels, n, groups
+    if brows != rows:
+        raise ValueError(f"B must have {rows} rows, got {brows}")
+    return (u.data_ptr(), _rows(u, "u", device, dtype, shape, channels),
+            dt.data_ptr(), _rows(dt, "dt", device, dt.dtype, shape, channels),
+            _whole(dt_bias, "dt_bias", device, torch.float32, (channels,)),
+            _whole(A, "A", device, torch.float32, (channels, n)),
+            B.data_ptr(), _rows(B, "B", device, dtype, bshape, groups * n),
+            C.data_ptr(), _rows(C, "C", device, dtype, bshape, groups * n),
+            _whole(D, "D", device, torch.float32, (channels,)),
+            None if z is None else z.data_ptr(), 0 if z is None else _rows(z, "z", device, dtype, shape, channels),
+            code, code if dt.dtype == dtype else _dtype_code(dt)), channels, n, groups
+
+
+def _slots(t: torch.Tensor, name: str, device, nseqs: int):
+    """A slot array as contiguous int32 on the device."""
+    if t.shape != (nseqs,):
+        raise ValueError(f"{name} must have shape {(nseqs,)}, got {tuple(t.shape)}")
+    if t.dtype == torch.int32 and t.device == device and t.is_contiguous():
+        return t
+    return _index(t, device)
 
 
 def selective_scan_varlen(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
@@ -550,26 +569,25 @@ def selective_scan_varlen(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B:
     `chunk_states` (float32 [slots, D, N]) receives the state after each chunk, at index c or at
     chunk_state_dst[c] when given. Returns (y, final_states)."""
     head, channels, n, groups = _selective_inputs(u, dt, A, B, C, dt_bias, D, z)
-    device = u.device
+    device, f32 = u.device, torch.float32
     if u.shape[0] != meta.total_tokens:
         raise ValueError(f"u has {u.shape[0]} tokens, the metadata {meta.total_tokens}")
     states = (meta.nseqs, channels, n)
     cap = 0 if chunk_states is None else chunk_states.shape[0]
-    _params(device, initial_states=(initial_states, states), final_states=(final_states, states),
-            chunk_states=(chunk_states, (cap, channels, n)))
-    if has_initial_state is not None:
-        _shape(has_initial_state, "has_initial_state", meta.nseqs)
-        has_initial_state = _index(has_initial_state, device)
+    init = _whole(initial_states, "initial_states", device, f32, states)
+    cst = _whole(chunk_states, "chunk_states", device, f32, (cap, channels, n))
+    has = None if has_initial_state is None else _slots(has_initial_state, "has_initial_state", device, meta.nseqs)
     _dst_len(chunk_state_dst, meta)
-    if chunk_state_dst is not None:
-        chunk_state_dst = _index(chunk_state_dst, device)
-    y, y_stride = _out_rows(y, "y", u)
+    dst = None if chunk_state_dst is None else _slots(chunk_state_dst, "chunk_state_dst", device,
+                                                      chunk_state_dst.numel())
+    y, y_stride = _out_rows(y, "y", u, channels)
     if final_states is None:
-        final_states = torch.empty(states, dtype=torch.float32, device=device)
+        final_states = torch.empty(states, dtype=f32, device=device)
     m = meta.c_struct()
-    _enqueue("ssd_selective_scan_varlen", device, *head, ctypes.byref(m), channels, n, groups,
-             _address(initial_states), _address(has_initial_state), y.data_ptr(), y_stride, final_states.data_ptr(),
-             _address(chunk_states), _address(chunk_state_dst), cap)
+    _enqueue("ssd_selective_scan_varlen", device, *head, ctypes.byref(m), channels, n, groups, init,
+             None if has is None else has.data_ptr(), y.data_ptr(), y_stride,
+             _whole(final_states, "final_states", device, f32, states), cst,
+             None if dst is None else dst.data_ptr(), cap)
     return y, final_states
 
 
@@ -582,16 +600,14 @@ def selective_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     written to state_cache[write_slot[s]] (skipped if < 0). u, dt, z (S, D), B, C (S, G, N), state_cache float32
     (slots, D, N). Returns y (S, D)."""
     head, channels, n, groups = _selective_inputs(u, dt, A, B, C, dt_bias, D, z)
-    device, nseqs = u.device, u.shape[0]
-    _params(device, state_cache=(state_cache, (state_cache.shape[0], channels, n)))
-    _shape(read_slot, "read_slot", nseqs)
-    _shape(write_slot, "write_slot", nseqs)
-    rs, ws = _index(read_slot, device), _index(write_slot, device)
-    if error_flag is not None:
-        _data(error_flag, "error_flag", device, torch.int32)
-    y, y_stride = _out_rows(y, "y", u)
-    _enqueue("ssd_selective_step", device, *head, nseqs, channels, n, groups, state_cache.data_ptr(),
-             state_cache.shape[0], rs.data_ptr(), ws.data_ptr(), y.data_ptr(), y_stride, _address(error_flag))
+    device, nseqs, slots = u.device, u.shape[0], state_cache.shape[0]
+    cache = _whole(state_cache, "state_cache", device, torch.float32, (slots, channels, n))
+    rs = _slots(read_slot, "read_slot", device, nseqs)
+    ws = _slots(write_slot, "write_slot", device, nseqs)
+    flag = _whole(error_flag, "error_flag", device, torch.int32, (1,))
+    y, y_stride = _out_rows(y, "y", u, channels)
+    _enqueue("ssd_selective_step", device, *head, nseqs, channels, n, groups, cache, slots, rs.data_ptr(),
+             ws.data_ptr(), y.data_ptr(), y_stride, flag)
     return y
 
 
@@ -605,25 +621,21 @@ def causal_conv1d_step(x: torch.Tensor, weight: torch.Tensor, conv_states: Optio
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError(f"x must be (sequences, channels) and weight (channels, width), got {tuple(x.shape)} and "
                          f"{tuple(weight.shape)}")
-    device = x.device
+    device, dtype, f32 = x.device, x.dtype, torch.float32
     nseqs, channels = x.shape
     width = weight.shape[1]
-    x_stride = _rows(x, "x", device, x.dtype, x.shape)
-    _params(device, weight=(weight, (channels, width)), bias=(bias, (channels,)))
-    if conv_states is not None:
-        _shape(conv_states, "conv_states", conv_states.shape[0], width - 1, channels)
-        _data(conv_states, "conv_states", device, x.dtype)
-    for name, t in (("read_slot", read_slot), ("write_slot", write_slot)):
-        _shape(t, name, nseqs)
-    rs = None if read_slot is None else _index(read_slot, device)
-    ws = None if write_slot is None else _index(write_slot, device)
-    if error_flag is not None:
-        _data(error_flag, "error_flag", device, torch.int32)
-    out, out_stride = _out_rows(out, "out", x)
-    _enqueue("ssd_causal_conv1d_step", device, x.data_ptr(), x_stride, weight.data_ptr(), _address(bias),
-             _dtype_code(x), nseqs, channels, width, int(bool(silu)), _address(conv_states),
-             0 if conv_states is None else conv_states.shape[0], _address(rs), _address(ws), out.data_ptr(),
-             out_stride, _address(error_flag))
+    slots = 0 if conv_states is None else conv_states.shape[0]
+    x_stride = _rows(x, "x", device, dtype, x.shape, channels)
+    w = _whole(weight, "weight", device, f32, (channels, width))
+    b = _whole(bias, "bias", device, f32, (channels,))
+    states = _whole(conv_states, "conv_states", device, dtype, (slots, width - 1, channels))
+    rs = None if read_slot is None else _slots(read_slot, "read_slot", device, nseqs)
+    ws = None if write_slot is None else _slots(write_slot, "write_slot", device, nseqs)
+    flag = _whole(error_flag, "error_flag", device, torch.int32, (1,))
+    out, out_stride = _out_rows(out, "out", x, channels)
+    _enqueue("ssd_causal_conv1d_step", device, x.data_ptr(), x_stride, w, b, _dtype_code(x), nseqs, channels, width,
+             1 if silu else 0, states, slots, None if rs is None else rs.data_ptr(),
+             None if ws is None else ws.data_ptr(), out.data_ptr(), out_stride, flag)
     return out
 
 
@@ -640,13 +652,14 @@ def group_norm(x: torch.Tensor, ngroups: int, weight: Optional[torch.Tensor] = N
         raise ValueError(f"act must be one of {sorted(NORM_ACTS)}, got {act!r}")
     if (z is not None) != act.startswith("gate"):
         raise ValueError("z is given exactly with the gated forms")
-    device = x.device
-    channels = x.shape[1:].numel()
-    x_stride = _rows(x, "x", device, x.dtype, x.shape)
-    z_stride = 0 if z is None else _rows(z, "z", device, x.dtype, x.shape)
-    _params(device, weight=(weight, (channels,)), bias=(bias, (channels,)))
-    out, out_stride = _out_rows(out, "out", x)
-    _enqueue("ssd_group_norm", device, x.data_ptr(), x_stride, _address(z), z_stride, _address(weight),
-             _address(bias), _dtype_code(x), x.shape[0], channels, int(ngroups), float(eps), int(bool(center)),
-             NORM_ACTS[act], out.data_ptr(), out_stride)
+    device, dtype, shape, f32 = x.device, x.dtype, x.shape, torch.float32
+    channels = shape[1] if len(shape) == 2 else shape[1:].numel()
+    x_stride = _rows(x, "x", device, dtype, shape, channels)
+    z_stride = 0 if z is None else _rows(z, "z", device, dtype, shape, channels)
+    w = _whole(weight, "weight", device, f32, (channels,))
+    b = _whole(bias, "bias", device, f32, (channels,))
+    out, out_stride = _out_rows(out, "out", x, channels)
+    _enqueue("ssd_group_norm", device, x.data_ptr(), x_stride, None if z is None else z.data_ptr(), z_stride, w, b,
+             _dtype_code(x), shape[0], channels, int(ngroups), float(eps), 1 if center else 0, NORM_ACTS[act],
+             out.data_ptr(), out_stride)
     return out
