@@ -109,14 +109,6 @@ __device__ __forceinline__ float sum_scatter4(const float (&y)[4]) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Sum over the four lanes 16 apart; every lane gets it.
-__device__ __forceinline__ float sum_lanes4(float v) {
-    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-
 template <typename T, typename DT, int N, int SEG>
 __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs a) {
     constexpr int NBLK = N / 16, J = SEG / 4;
@@ -158,13 +150,19 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
     float *ldsC = mine + SEG * 48;
 
     const int64_t state_row = (int64_t)s * a.C_total * N;
-    const int64_t state_col = (int64_t)d * N + 4 * q;
     float *final = a.final_states + state_row;
+    // The lane's place in a state. Computed anew at each of its rare uses (as is all that only a sequence's last segment
+    // needs): kept over the segments, such values push others out to memory.
+    auto state_col = [&] {
+        int channel = d;
+        asm volatile("" : "+v"(channel));
+        return (int64_t)channel * N + 4 * q;
+    };
     const bool start = a.init != nullptr && (a.has_init == nullptr || a.has_init[s] != 0);
     for (int nb = wave; nb < NBLK; nb += nw) {
-        const f32x4 h = start ? *reinterpret_cast<const f32x4 *>(a.init + state_row + nb * 16 + state_col) : f32x4{0, 0, 0, 0};
+        const f32x4 h = start ? *reinterpret_cast<const f32x4 *>(a.init + state_row + nb * 16 + state_col()) : f32x4{0, 0, 0, 0};
         *reinterpret_cast<f32x4 *>(carry + (nb * 64 + lane) * 4) = h;
-        if (nseg == 0) *reinterpret_cast<f32x4 *>(final + nb * 16 + state_col) = h;
+        if (nseg == 0) *reinterpret_cast<f32x4 *>(final + nb * 16 + state_col()) = h;
         if (lane == 0) done[nb] = 0;
     }
     __syncthreads();
@@ -217,12 +215,14 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
         fetch_bc(SEG, 0);
     };
     auto fetch_rest = [&](int rows) {   // a segment of fewer: past the end, the last token again
+        int d_ = d, q_ = q;
+        asm volatile("" : "+v"(d_), "+v"(q_));
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const uint32_t r = min(4 * j + q, rows - 1);
-            ru[j] = *reinterpret_cast<const One *>(pu + (r * (uint32_t)su + d * ES));
-            rd[j] = *reinterpret_cast<const OneD *>(pd + (r * (uint32_t)sd + d * ED));
-            rz[j] = *reinterpret_cast<const One *>(pz + (r * (uint32_t)sz + d * ES));
+            const uint32_t r = min(4 * j + q_, rows - 1);
+            ru[j] = *reinterpret_cast<const One *>(pu + (r * (uint32_t)su + d_ * ES));
+            rd[j] = *reinterpret_cast<const OneD *>(pd + (r * (uint32_t)sd + d_ * ED));
+            rz[j] = *reinterpret_cast<const One *>(pz + (r * (uint32_t)sz + d_ * ES));
         }
         fetch_bc(rows, 0);
     };
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
                 slot = -1;
             }
         }
-        float u[J], sum = 0.0f;
+        float u[J];
         One z[J];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
@@ -250,10 +250,8 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
             z[j] = rz[j];
             float delta = softplus_full(RD::f(rd[j]) + bias), du = delta * u[j];
             if (!FULL && 4 * j + q >= left) delta = du = 0.0f;
-            sum += delta;
             *reinterpret_cast<f32x2 *>(ldsD + ((4 * j + q) * 16 + c) * 2) = f32x2{delta, du};
         }
-        sum = sum_lanes4(sum);
 
         auto emit = [&](int j, const float (&part)[4]) {   // tokens 4 j .. 4 j + 3
             float v = fmaf(skip, u[j], sum_scatter4(part));
@@ -283,53 +281,40 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
             }
             __builtin_amdgcn_wave_barrier();
 
-            // LDS values of the next tokens are on their way while these are computed (the compiler, left alone, either
-            // waits for each read or reads everything ahead and spills)
-            constexpr int G1 = 4, G2 = 2;   // tokens of a read group in the two passes
-            f32x4 dec[SEG], h = {0, 0, 0, 0};
-            f32x2 dd[2][G1];
-            float bt[2][G1];
-            auto read1 = [&](int grp) {
-#pragma unroll
-                for (int k = 0; k < G1; ++k) {
-                    const int t = grp * G1 + k;
-                    dd[grp & 1][k] = *reinterpret_cast<const f32x2 *>(ldsD + (t * 16 + c) * 2);
-                    bt[grp & 1][k] = ldsB[t * 16 + 4 * q + (lane & 3)];
-                }
+            // LDS values of the next token are on their way while one is computed (the compiler, left alone, either waits
+            // for each read or reads everything ahead and spills)
+            constexpr int G2 = 2;   // tokens of a read group in the second pass
+            f32x4 dec[SEG], inp[SEG], h, p;
+            f32x2 dd[2];
+            f32x4 bv[2];
+            auto read1 = [&](int t) {
+                dd[t & 1] = *reinterpret_cast<const f32x2 *>(ldsD + (t * 16 + c) * 2);
+                bv[t & 1] = *reinterpret_cast<const f32x4 *>(ldsB + t * 16 + 4 * q);
             };
             read1(0);
 #pragma unroll
-            for (int grp = 0; grp < SEG / G1; ++grp) {
-                if (grp + 1 < SEG / G1) read1(grp + 1);
+            for (int t = 0; t < SEG; ++t) {
+                if (t + 1 < SEG) read1(t + 1);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int k = 0; k < G1; ++k) {
-                    const int t = grp * G1 + k;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        dec[t][i] = fast_exp2(dd[grp & 1][k][0] * rate[i]);
-                        if (t > 0) h[i] *= dec[t][i];
-                    }
-                    h = __builtin_amdgcn_mfma_f32_4x4x1f32(bt[grp & 1][k], dd[grp & 1][k][1], h, 0, 0, 0);
+                for (int i = 0; i < 4; ++i) {
+                    dec[t][i] = fast_exp2(dd[t & 1][0] * rate[i]);
+                    inp[t][i] = dd[t & 1][1] * bv[t & 1][i];
+                    h[i] = t == 0 ? inp[t][i] : fmaf(dec[t][i], h[i], inp[t][i]);
+                    p[i] = t == 0 ? dec[t][i] : p[i] * dec[t][i];
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            float du2[2][G2], bt2[2][G2];
             f32x4 cv[2][G2];
             auto read2 = [&](int grp) {
 #pragma unroll
-                for (int k = 0; k < G2; ++k) {
-                    const int t = grp * G2 + k;
-                    du2[grp & 1][k] = ldsD[(t * 16 + c) * 2 + 1];
-                    bt2[grp & 1][k] = ldsB[t * 16 + 4 * q + (lane & 3)];
-                    cv[grp & 1][k] = *reinterpret_cast<const f32x4 *>(ldsC + t * 16 + 4 * q);
-                }
+                for (int k = 0; k < G2; ++k)
+                    cv[grp & 1][k] = *reinterpret_cast<const f32x4 *>(ldsC + (grp * G2 + k) * 16 + 4 * q);
             };
             read2(0);
-            f32x4 p;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = fast_exp2(sum * rate[i]);
-            asm volatile("" : "+v"(p));        // before the wait, not after it
+            for (int t = 0; t < SEG; ++t) asm volatile("" : "+v"(dec[t]), "+v"(inp[t]));   // before the wait, not after it
+            asm volatile("" : "+v"(p), "+v"(h));
             __builtin_amdgcn_s_setprio(2);     // the other waves wait for what follows
 
             // the chain: segment seg's wave is the only one that touches the buffer between done = seg and seg + 1.
@@ -353,10 +338,10 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
             asm volatile("" ::: "memory");
             if (slot >= 0) {
                 float *to = a.chunk_states + (int64_t)slot * a.C_total * N + nb * 16;   // uniform
-                *reinterpret_cast<f32x4 *>(to + state_col) = h;
+                *reinterpret_cast<f32x4 *>(to + state_col()) = h;
             }
             if (!FULL || left == SEG) {
-                *reinterpret_cast<f32x4 *>(final + nb * 16 + state_col) = h;
+                *reinterpret_cast<f32x4 *>(final + nb * 16 + state_col()) = h;
             }
 
 #pragma unroll
@@ -368,15 +353,14 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
                     const int t = grp * G2 + k;
                     const f32x4 ct = cv[grp & 1][k];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) in[i] *= dec[t][i];
-                    in = __builtin_amdgcn_mfma_f32_4x4x1f32(bt2[grp & 1][k], du2[grp & 1][k], in, 0, 0, 0);
+                    for (int i = 0; i < 4; ++i) in[i] = fmaf(dec[t][i], in[i], inp[t][i]);
                     float v = NBLK > 1 ? fmaf(in[0], ct[0], y[NBLK > 1 ? t : 0]) : in[0] * ct[0];
 #pragma unroll
                     for (int i = 1; i < 4; ++i) v = fmaf(in[i], ct[i], v);
                     y[NBLK > 1 ? t : t & 3] = v;
                 }
                 if constexpr (NBLK == 1) {
-                    if (grp & 1) emit(grp / 2, {y[0], y[1], y[2], y[3]});
+                    if ((grp + 1) * G2 % 4 == 0) emit((grp + 1) * G2 / 4 - 1, {y[0], y[1], y[2], y[3]});
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
