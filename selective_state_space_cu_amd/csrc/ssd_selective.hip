@@ -6,9 +6,7 @@
 // The decay differs per (token, channel, state), so a chunk has no form as a
 // matrix product (a per-head decay has one): what there is to compute is one
 // exponential and a few products and sums per (token, channel, state).
-//
-// Lanes: a wave owns 16 channels; lane = 16 q + c holds the states
-// n = q N/4 .. (q + 1) N/4 - 1 of channel c.
+// (delta is scaled by log2 e, not A: delta = 0 leaves the state for any finite A.)
 #include <type_traits>
 
 #include "ssd_scan.hpp"
@@ -43,29 +41,39 @@ template <typename T> __device__ __forceinline__ float load_f(const void *p, int
 }
 
 // ---------------------------------------------------------------------------
-// Scan. A workgroup owns 16 channels of one sequence; its TW waves take
-// segments of SEG tokens in turn (wave w: segments w, w + TW, ...). A
-// segment is an affine map of the state, h -> P h + e, and only that map's use
-// is serial:
-//   pass 1 (any time): the decays a_t = 2^(delta_t A log2 e), kept in registers,
-//     and e, the state after the segment from a zero state; P = 2^(A log2 e sum delta_t);
+// Scan, in segments. A workgroup owns 16 channels of one sequence; its waves take
+// segments of kSeg tokens in turn (wave w of W: segments w, w + W, ...). A segment
+// is an affine map of the state, h -> P h + e, and only that map's use is serial:
+//   pass 1 (any time): the decays a_t = 2^(delta_t A log2 e) and the inputs
+//     b_t = delta_t u_t B_t, kept in registers; e, the state after the segment
+//     from a zero state; P, the product of the a_t;
 //   chain (in order): wait for the state h_in that enters the segment, publish
 //     P h_in + e for the next segment's wave;
 //   pass 2: h_t = a_t h_(t-1) + b_t again from h_in, and y_t = h_t . C_t.
-// The exponentials, which cost most, are computed once; the price of running
-// TW segments side by side is one product and the outer product b_t a second
-// time. The chain runs through LDS: one state buffer, which each segment's wave
-// reads and then overwrites, and a counter of finished segments.
+// The exponentials, which cost most, are computed once; the price of running W
+// segments side by side is one product and one sum more. The chain runs through
+// LDS: one state buffer, which each segment's wave reads and then overwrites, and
+// a counter of finished segments. Every wave of the workgroup is resident and
+// takes its segments in order, so the wave that the others wait for never waits
+// for them: every wait ends.
 //
 // Lanes: lane = 16 q + c holds the states n = 16 nb + 4 q + i (i < 4) of channel
-// c, for one block nb of 16 states at a time. b_t = (delta_t u_t) B_t is an
-// outer product of 16 channels and 16 states: one v_mfma_f32_4x4x1 (16 blocks
-// of 4x4; lane l gives B_t[4 q + l % 4] and delta_t u_t of its channel, and
-// receives the four b of its own states on top of the a h it passes as the sum).
-// What is per (token, channel) only - softplus, gate, loads, stores - is done
-// by lane (q, c) for the tokens 4 j + q, so nothing is computed four times;
-// delta and delta u reach the other lanes through LDS, and the four partial
-// sums of y_t come back by three half swaps per four tokens.
+// c, for one block nb of 16 states at a time. What is per (token, channel) only -
+// softplus, gate, loads, stores - is done by lane (q, c) for the tokens 4 j + q,
+// so nothing is computed four times; delta and delta u reach the other lanes
+// through LDS, as B_t and C_t do, and the four partial sums of y_t come back by
+// three half swaps per four tokens.
+//
+// What bounds it: instruction issue. Per token and 16 channels x 16 states a wave
+// issues 4 exponentials (3.4 ns of a SIMD each), 20 products and sums (about 1 ns
+// with vector operands and an even number of waves) and its share of the rest, 56
+// ns in all; 80 are measured (4 x 8894 tokens, 4096 channels: 712 us, 1.7 TB/s),
+// the difference being LDS (half of its time taken) and waits.
+// Tried and slower: b_t as an outer product on v_mfma_f32_4x4x1 (it holds the
+// vector unit for 5 ns and saves 4 products), 64 channels to a wave with B and C as
+// scalar operands (each such product takes twice as long), 16 tokens to a segment
+// or 5 waves a SIMD (the decays no longer fit the registers).
+constexpr int kSeg = 8;    // tokens of a segment
 constexpr int kCh = 16;    // channels of a workgroup
 
 template <typename T> struct RawOf;
@@ -109,9 +117,9 @@ __device__ __forceinline__ float sum_scatter4(const float (&y)[4]) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-template <typename T, typename DT, int N, int SEG>
+template <typename T, typename DT, int N>
 __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs a) {
-    constexpr int NBLK = N / 16, J = SEG / 4;
+    constexpr int NBLK = N / 16, SEG = kSeg, J = SEG / 4;
     using R = RawOf<T>;
     using RD = RawOf<DT>;
     using One = typename R::One;
@@ -121,10 +129,9 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
     extern __shared__ __attribute__((aligned(16))) float lds[];
     if (__builtin_nontemporal_load(a.error_flag) & SSD_DATA_BAD_CU_SEQLENS) return;
     const int per = a.C_total / a.G, bpg = (per + kCh - 1) / kCh, cblocks = a.G * bpg;   // blocks stay inside a group
-    // four neighbouring channel blocks (one 128-byte line of bf16) on one XCD
-    const int total = (int)gridDim.x;
+    // four neighbouring channel blocks (one 128-byte line of bf16) on one XCD: blocks go to the 8 XCDs in turn
     int b = blockIdx.x;
-    if ((b | 31) < total) b = (b & ~31) | ((b & 7) << 2) | ((b >> 3) & 3);
+    if ((b | 31) < (int)gridDim.x) b = (b & ~31) | ((b & 7) << 2) | ((b >> 3) & 3);
     const int rank = b / cblocks, cb = b - rank * cblocks;
     const int s = a.seq_order[rank];
     if (s < 0 || s >= a.S) return;
@@ -145,7 +152,7 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
     float *carry = lds;                                           // [NBLK][64][4]
     lds_counter *done = (lds_counter *)(__attribute__((address_space(3))) int *)(lds + NBLK * 256);   // [NBLK] segments finished
     float *mine = lds + NBLK * 256 + ((NBLK + 3) & ~3) + wave * (SEG * 64);
-    float *ldsD = mine;                 // [SEG tokens][16 channels] (delta, delta u)
+    float *ldsD = mine;                 // [SEG tokens][16 channels] (delta log2 e, delta u)
     float *ldsB = mine + SEG * 32;      // [SEG tokens][16 states]
     float *ldsC = mine + SEG * 48;
 
@@ -169,7 +176,7 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
     if (wave >= nseg) return;
 
     const float bias = a.dt_bias != nullptr ? a.dt_bias[d] : 0.0f, skip = a.D != nullptr ? a.D[d] : 0.0f;
-    f32x4 rate = *reinterpret_cast<const f32x4 *>(a.A + (int64_t)d * N + 4 * q) * kLog2e;
+    f32x4 rate = *reinterpret_cast<const f32x4 *>(a.A + (int64_t)d * N + 4 * q) ;
 
     // Addresses: uniform pointers to the first row of a segment, advanced from segment to segment, plus 32-bit lane
     // offsets (the API's bound on strides keeps 16 rows below 2^32 bytes).
@@ -182,28 +189,23 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
     char *py = reinterpret_cast<char *>(a.y) + first * sy;
     const uint32_t offU = q * (uint32_t)su + d * ES, offD = q * (uint32_t)sd + d * ED, offZ = q * (uint32_t)sz + d * ES,
                    offY = q * (uint32_t)sy + d * ES;
-    // B and C: every lane its own token and four states, through a pointer of its own
+    // B and C: every lane four states of one token, lanes 0 .. 31 of B and the others of C, through a pointer of its own
     const int tokBC = lane >> 2 & (SEG - 1);
-    const bool holdsB = SEG == 16 || lane < 32;
-    const int64_t sBC = holdsB ? sB : sC;
-    const char *pBC = (holdsB ? reinterpret_cast<const char *>(a.B) : reinterpret_cast<const char *>(a.C)) +
-                      (first + tokBC) * sBC + (g * N + 4 * (lane & 3)) * ES;
-    const char *pC = SEG == 16 ? reinterpret_cast<const char *>(a.C) + (first + tokBC) * sC + (g * N + 4 * (lane & 3)) * ES
-                               : nullptr;
+    const int64_t sBC = lane < 32 ? sB : sC;
+    const char *pBC = reinterpret_cast<const char *>(lane < 32 ? a.B : a.C) + (first + tokBC) * sBC +
+                      (g * N + 4 * (lane & 3)) * ES;
 
     // bytes from a wave's segment to its next
     const int64_t ahead = (int64_t)nw * SEG, nextU = ahead * su, nextD = ahead * sd, nextZ = ahead * sz, nextY = ahead * sy,
-                  nextBC = ahead * sBC, nextC = ahead * sC;
+                  nextBC = ahead * sBC;
 
-    // raw inputs of a segment, fetched one segment ahead: tokens 4 j + q of channel c; four states of B and C of one
-    // token (SEG = 8: 32 lanes hold B, the others C; SEG = 16: every lane holds both)
+    // raw inputs of a segment, fetched one segment ahead
     One ru[J], rz[J];
     OneD rd[J];
-    Four rB, rC;
+    Four rBC;
     auto fetch_bc = [&](int rows, int nb) {   // rows past the end: the last one
         const int64_t back = max(tokBC - (rows - 1), 0);
-        rB = *reinterpret_cast<const Four *>(pBC + nb * 16 * ES - (rows >= SEG ? 0 : back * sBC));
-        if constexpr (SEG == 16) rC = *reinterpret_cast<const Four *>(pC + nb * 16 * ES - (rows >= SEG ? 0 : back * sC));
+        rBC = *reinterpret_cast<const Four *>(pBC + nb * 16 * ES - (rows >= SEG ? 0 : back * sBC));
     };
     auto fetch = [&] {   // a segment of SEG tokens
 #pragma unroll
@@ -248,9 +250,8 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
         for (int j = 0; j < J; ++j) {
             u[j] = R::f(ru[j]);
             z[j] = rz[j];
-            float delta = softplus_full(RD::f(rd[j]) + bias), du = delta * u[j];
-            if (!FULL && 4 * j + q >= left) delta = du = 0.0f;
-            *reinterpret_cast<f32x2 *>(ldsD + ((4 * j + q) * 16 + c) * 2) = f32x2{delta, du};
+            const float delta = softplus_full(RD::f(rd[j]) + bias);
+            *reinterpret_cast<f32x2 *>(ldsD + ((4 * j + q) * 16 + c) * 2) = f32x2{delta * kLog2e, delta * u[j]};
         }
 
         auto emit = [&](int j, const float (&part)[4]) {   // tokens 4 j .. 4 j + 3
@@ -266,9 +267,8 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
 
 #pragma unroll 1
         for (int nb = 0; nb < NBLK; ++nb) {
-            *reinterpret_cast<f32x4 *>(ldsB + lane * 4) = R::f4(rB);   // (SEG = 8: C follows B)
-            if constexpr (SEG == 16) *reinterpret_cast<f32x4 *>(ldsC + lane * 4) = R::f4(rC);
-            if (NBLK > 1) rate = *reinterpret_cast<const f32x4 *>(a.A + (int64_t)d * N + nb * 16 + 4 * q) * kLog2e;
+            *reinterpret_cast<f32x4 *>(ldsB + lane * 4) = R::f4(rBC);   // C follows B
+            if (NBLK > 1) rate = *reinterpret_cast<const f32x4 *>(a.A + (int64_t)d * N + nb * 16 + 4 * q);
             if (nb + 1 < NBLK) {
                 fetch_bc(FULL ? SEG : left, nb + 1);
             } else if (FULL) {
@@ -276,7 +276,6 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
                 pd += nextD;
                 pz += nextZ;
                 pBC += nextBC;
-                if (SEG == 16) pC += nextC;
                 if (left >= (nw + 1) * SEG) fetch();
             }
             __builtin_amdgcn_wave_barrier();
@@ -300,6 +299,10 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
                 for (int i = 0; i < 4; ++i) {
                     dec[t][i] = fast_exp2(dd[t & 1][0] * rate[i]);
                     inp[t][i] = dd[t & 1][1] * bv[t & 1][i];
+                    if (!FULL && t >= left) {   // past the end (uniform): the state stays
+                        dec[t][i] = 1.0f;
+                        inp[t][i] = 0.0f;
+                    }
                     h[i] = t == 0 ? inp[t][i] : fmaf(dec[t][i], h[i], inp[t][i]);
                     p[i] = t == 0 ? dec[t][i] : p[i] * dec[t][i];
                 }
@@ -383,7 +386,12 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
 // chain go. A wave owns 64 channels, lane = channel with all N states, and takes
 // token after token. B_t and C_t are the same for all lanes: they come through the
 // scalar cache into scalar registers, which the products take as operands (their
-// rows have to lie on 4-byte boundaries). Inputs are fetched K tokens ahead.
+// rows have to lie on 4-byte boundaries). Inputs are fetched K tokens ahead (2 and
+// 4 tokens: 461 and 473 us).
+// Bound by instruction issue: 16 exponentials (3.4 ns of a SIMD), 32 products with a
+// scalar operand (1.9 ns) and about 60 others (1 ns) a token, 172 ns in all; 220 are
+// measured (64 prompts of 8192 channels, 470 us, 2.6 TB/s). B and C as vector operands
+// from LDS took as long: twice the registers, half the waves.
 template <typename T, typename DT, int N, int K>
 __global__ __launch_bounds__(64) void ssd_selective_walk_kernel(SelectiveArgs a) {
     using R = RawOf<T>;
@@ -413,7 +421,7 @@ __global__ __launch_bounds__(64) void ssd_selective_walk_kernel(SelectiveArgs a)
         const f32x4 v = start ? *reinterpret_cast<const f32x4 *>(a.init + state_row + state_col + n) : f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            rate[n + i] = r[i] * kLog2e;
+            rate[n + i] = r[i];
             h[n + i] = v[i];
         }
     }
@@ -456,13 +464,14 @@ __global__ __launch_bounds__(64) void ssd_selective_walk_kernel(SelectiveArgs a)
         for (int i = 0; i < W; ++i) wB[i] = ((scalar_words *)pB)[i];
 #pragma unroll
         for (int i = 0; i < W; ++i) wC[i] = ((scalar_words *)pC)[i];
-        const float u = R::f(ru[k]), delta = softplus_full(RD::f(rd[k]) + bias), du = delta * u;
+        const float u = R::f(ru[k]), delta = softplus_full(RD::f(rd[k]) + bias), du = delta * u,
+                    delta2 = delta * kLog2e;
         const One z = rz[k];
         fetch(k);
         float y[2] = {skip * u, 0.0f};
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            h[n] = fmaf(fast_exp2(delta * rate[n]), h[n], du * value(wB, n));
+            h[n] = fmaf(fast_exp2(delta2 * rate[n]), h[n], du * value(wB, n));
             y[n & 1] = fmaf(h[n], value(wC, n), y[n & 1]);
         }
         float v = y[0] + y[1];
@@ -538,20 +547,21 @@ __global__ __launch_bounds__(kSelStepThreads) void ssd_selective_step_kernel(Sel
         }
         if (rs >= 0) h[k] = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(a.cache + rs * slot + at));
     }
-    const f32x4 rate = *reinterpret_cast<const f32x4 *>(a.A + at) * kLog2e;
+    const f32x4 rate = *reinterpret_cast<const f32x4 *>(a.A + at);
     const float bias = a.dt_bias != nullptr ? a.dt_bias[d] : 0.0f, skip = a.D != nullptr ? a.D[d] : 0.0f;
 #pragma unroll
     for (int k = 0; k < SEQS; ++k) {
         if (!taken[k]) continue;
         const int64_t s = sg * SEQS + k;
         const float u = load_f<T>(a.u, s * a.u_stride + d);
-        const float delta = softplus_full(load_f<DT>(a.dt, s * a.dt_stride + d) + bias), du = delta * u;
+        const float delta = softplus_full(load_f<DT>(a.dt, s * a.dt_stride + d) + bias), du = delta * u,
+                    delta2 = delta * kLog2e;
         const f32x4 bv = R::f4(*reinterpret_cast<const typename R::Four *>(reinterpret_cast<const T *>(a.B) + s * a.B_stride + n0));
         const f32x4 cv = R::f4(*reinterpret_cast<const typename R::Four *>(reinterpret_cast<const T *>(a.C) + s * a.C_stride + n0));
         float y = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            h[k][i] = fmaf(fast_exp2(delta * rate[i]), h[k][i], du * bv[i]);
+            h[k][i] = fmaf(fast_exp2(delta2 * rate[i]), h[k][i], du * bv[i]);
             y = fmaf(h[k][i], cv[i], y);
         }
         if (ws[k] >= 0) __builtin_nontemporal_store(h[k], reinterpret_cast<f32x4 *>(a.cache + ws[k] * slot + at));
@@ -566,14 +576,16 @@ __global__ __launch_bounds__(kSelStepThreads) void ssd_selective_step_kernel(Sel
 }
 
 // Waves of a workgroup that splits sequences into segments: the fewer (sequence,
-// 16 channels) pairs there are, the more. 2560 pairs (8 ragged prompts): 4 waves
-// 374 us, 8 waves 388, 16 waves 476; 1024 pairs (4 x 8894 tokens): 745, 730, 793;
-// 160 pairs (one prompt of 30001 tokens): 1071, 718, 649.
-static int segment_waves(int64_t pairs) { return pairs >= 1024 ? 4 : pairs >= 512 ? 8 : 16; }
+// 16 channels) pairs there are, the more. Microseconds with 2 / 4 / 8 / 16 waves:
+// 16384 pairs (64 x 300 tokens) 375 / 395; 2560 (8 ragged prompts) 424 / 376 /
+// 392 / 448; 1024 (4 x 8894 tokens) 823 / 737 / 712 / 752; 160 (one prompt of
+// 30001 tokens) 2069 / 987 / 633 / 541.
+static int segment_waves(int64_t pairs) { return pairs >= 8192 ? 2 : pairs >= 2048 ? 4 : pairs >= 512 ? 8 : 16; }
 
 // From this many (sequence, 64 channels) pairs on, 4 for every SIMD, sequences
-// are walked (64 prompts of 1 to 490 tokens, 8192 channels: 690 us in segments,
-// 460 walked; 8 prompts of 5120 channels, 640 pairs: 390 and 2150).
+// are walked (64 prompts of 3 to 490 tokens, 8192 channels, 8192 pairs: 665 us in
+// segments, 470 walked; 4096 channels: 64 x 300 tokens, 4096 pairs, 375 and 354;
+// 32 x 500 tokens 319 and 399; 16 x 1000 tokens 322 and 630).
 constexpr int64_t kWalkPairs = 4096;
 // A walk takes as long as its sequence, so one much longer than the others would
 // be left over: those of more than 3 times the mean length go in segments.
@@ -585,15 +597,14 @@ constexpr int kStepSeqs = 2;
 constexpr int64_t kStepFill = 2048;
 
 template <typename T, typename DT, int N> struct SelectiveLaunch {
-    static constexpr int SEG = 8;   // tokens of a segment (16: 128 registers do not hold the decays, 872 us against 771)
     // Sequences of more than a.walk_to tokens, among the `ranks` longest, in segments.
     static hipError_t segments(const SelectiveArgs &a, int64_t ranks, hipStream_t stream) {
         const int64_t blocks = ranks * a.G * ((a.C_total / a.G + kCh - 1) / kCh);
         const int waves = segment_waves(blocks);
         if (!fits_grid(blocks, 64 * waves)) return hipErrorInvalidConfiguration;
         constexpr int NBLK = N / 16;
-        const size_t lds = sizeof(float) * (NBLK * 256 + ((NBLK + 3) & ~3) + (size_t)waves * SEG * 64);
-        hipLaunchKernelGGL((ssd_selective_scan_kernel<T, DT, N, SEG>), dim3((unsigned)blocks), dim3(64 * waves), lds,
+        const size_t lds = sizeof(float) * (NBLK * 256 + ((NBLK + 3) & ~3) + (size_t)waves * kSeg * 64);
+        hipLaunchKernelGGL((ssd_selective_scan_kernel<T, DT, N>), dim3((unsigned)blocks), dim3(64 * waves), lds,
                            stream, a);
         return hipGetLastError();
     }

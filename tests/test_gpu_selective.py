@@ -452,3 +452,49 @@ def test_scan_of_many_sequences_with_odd_rows():
     ry, rh, by, bh, _ = expected(j)[0]
     ref.check(y[r], ry, by, "y")
     ref.check(fin[150], rh[-1], bh[-1], "state")
+
+
+@pytest.mark.parametrize("path", ["segments", "walk", "step"])
+def test_extreme_rates_and_infinite_inputs(path):
+    """Rates of the type's lowest value and of minus infinity (the state is replaced, but a step size of zero leaves it
+    for any finite rate), and an infinite B at a sequence's ragged end, which reaches its own state and no other."""
+    n, d = 16, 1040 if path == "walk" else 48
+    lengths = [13] * 256 if path == "walk" else [1, 1] if path == "step" else [13, 5]
+    i = make(lengths, d, n, 1, F32, gate=False, init="all", seed=51, skip=False)
+    wide = torch.cat([i["B"].reshape(-1, n), i["C"].reshape(-1, n)], 1).contiguous()
+    i["B"], i["C"] = wide[:, :n].unflatten(1, (1, n)), wide[:, n:].unflatten(1, (1, n))
+    i["A"][1] = torch.finfo(F32).min
+    i["A"][2, 3] = float("-inf")
+    i["dt"][:, 1] = float("-inf")     # step sizes of zero for the channel of lowest rates
+    i["dt"][:, 2] = 1.0
+    last = lengths[0] - 1
+    i["B"][last, 0, 5] = float("inf")
+    i["u"][last, 7] = -1.5
+    if path == "step":
+        cache = torch.zeros(4, d, n, device="cuda")
+        cache[:2] = i["init"]
+        slots = torch.arange(4, dtype=torch.int32, device="cuda")
+        ssd.selective_step(i["u"], i["dt"], i["A"], i["B"], i["C"], cache, slots[:2], slots[2:], dt_bias=i["dt_bias"])
+        torch.cuda.synchronize()
+        fin = cache[2:]
+    else:
+        fin = call(i, chunk=16)[1]
+    c = {k: v.double() if isinstance(v, torch.Tensor) and v.is_floating_point() else v for k, v in cpu(i).items()}
+    delta = ref.softplus(c["dt"].clamp(min=-1e30) + c["dt_bias"])
+    t = 0
+    for s in range(2):
+        h = c["init"][s]
+        for _ in range(lengths[s]):
+            h = torch.exp(delta[t][:, None] * c["A"]) * h + (delta[t] * c["u"][t])[:, None] * c["B"][t]
+            t += 1
+        got = fin[s].cpu().double()
+        # channel 1 and state 5 of zero steps: 0 x inf
+        assert torch.equal(torch.isnan(got), torch.isnan(h)) and torch.equal(torch.isinf(got), torch.isinf(h))
+        assert torch.equal(got[torch.isinf(h)], h[torch.isinf(h)])
+        keep = torch.isfinite(h)
+        # up to 13 tokens: each state is good to about 13 x 50 units of 2^-24 of the largest term, 4e-5 at most
+        assert (got[keep] - h[keep]).abs().max() < 4e-5 * h[keep].abs().max()
+        if s == 0:
+            free = [k for k in range(n) if k != 5]
+            assert torch.equal(got[1][free], c["init"][0][1][free]), "a step size of zero changed a state"
+            assert got[7, 5] == float("-inf")
