@@ -216,15 +216,13 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
         }
         fetch_bc(SEG, 0);
     };
-    auto fetch_rest = [&](int rows) {   // a segment of fewer: past the end, the last token again
-        int d_ = d, q_ = q;
-        asm volatile("" : "+v"(d_), "+v"(q_));
+    auto fetch_rest = [&](int rows, int q, int d) {   // a segment of fewer: past the end, the last token again
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const uint32_t r = min(4 * j + q_, rows - 1);
-            ru[j] = *reinterpret_cast<const One *>(pu + (r * (uint32_t)su + d_ * ES));
-            rd[j] = *reinterpret_cast<const OneD *>(pd + (r * (uint32_t)sd + d_ * ED));
-            rz[j] = *reinterpret_cast<const One *>(pz + (r * (uint32_t)sz + d_ * ES));
+            const uint32_t r = min(4 * j + q, rows - 1);
+            ru[j] = *reinterpret_cast<const One *>(pu + (r * (uint32_t)su + d * ES));
+            rd[j] = *reinterpret_cast<const OneD *>(pd + (r * (uint32_t)sd + d * ED));
+            rz[j] = *reinterpret_cast<const One *>(pz + (r * (uint32_t)sz + d * ES));
         }
         fetch_bc(rows, 0);
     };
@@ -232,8 +230,12 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
 
     auto segment = [&](int seg, auto whole) {
         constexpr bool FULL = decltype(whole)::value;   // all SEG tokens exist
+        // (the sequence's last segment works its places out anew: kept, they would not fit beside the loop's)
+        int here = lane;
+        if constexpr (!FULL) asm volatile("" : "+v"(here));
+        const int q = here >> 4, c = here & 15, d = g * per + min((cb - g * bpg) * kCh + c, per - 1), lane = here;
         const int left = L - seg * SEG;                 // tokens from the segment's first on
-        if constexpr (!FULL) fetch_rest(left);          // once a sequence: not ahead
+        if constexpr (!FULL) fetch_rest(left, q, d);    // once a sequence: not ahead
         // the slot that receives the state after this segment, if a chunk ends here
         int slot = -1;
         if (a.chunk_states != nullptr && (!FULL || left == SEG || ((seg + 1) & (chunk_segs - 1)) == 0)) {
