@@ -233,3 +233,39 @@ def test_layer_of_prompts_then_tokens():
         off = (rows[s].cpu().double() - want).abs().max() / want.abs().max()
         assert off < 1e-5, f"sequence {s}: {off:.2e}"
         assert ((cache[int(slots[s])].cpu().double() - rh[-1]).abs().max() / rh[-1].abs().max()) < 1e-5
+
+
+def test_conv_step_and_norm_offsets_past_32_bits():
+    """A cache of 2^31 and more elements, and rows 2^26 elements apart."""
+    i = conv_inputs(3, 64, 4, BF, seed=70)
+    slots = 2 ** 31 // (3 * 64) + 20
+    cache = torch.empty(slots, 3, 64, dtype=BF, device="cuda")
+    high = torch.tensor([slots - 1, slots - 5, 2], dtype=torch.int32, device="cuda")
+    to = torch.tensor([slots - 2, slots - 6, slots - 9], dtype=torch.int32, device="cuda")
+    cache[high.long()] = i["states"][:3]
+    before = i["states"].clone()
+    i["read"], i["write"] = torch.arange(3, dtype=torch.int32).cuda(), torch.arange(3, 6, dtype=torch.int32).cuda()
+    want = ssd.causal_conv1d_step(i["x"], i["weight"], i["states"], i["read"], i["write"], bias=i["bias"])
+    out = ssd.causal_conv1d_step(i["x"], i["weight"], cache, high, to, bias=i["bias"])
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(cache[to.long()], i["states"][3:6])
+    assert torch.equal(i["states"][:3], before[:3])
+    far = torch.empty(40 * 2 ** 26, dtype=BF, device="cuda")
+    x, z, o = (far.as_strided((40, 96), (2 ** 26, 1), k * 128) for k in range(3))
+    n = norm_inputs(40, 96, BF, "gate_last", seed=71)
+    x.copy_(n["x"])
+    z.copy_(n["z"])
+    ssd.group_norm(x, 3, weight=n["weight"], z=z, act="gate_last", out=o)
+    torch.cuda.synchronize()
+    assert torch.equal(o, ssd.group_norm(n["x"], 3, weight=n["weight"], z=n["z"], act="gate_last"))
+
+
+def test_norm_of_more_groups_than_teams_fill_the_card():
+    """Many tiny groups, more than the teams of one launch: every (row, group) is visited once."""
+    i = norm_inputs(3, 2 ** 21, F32, "silu", seed=72)
+    got = ssd.group_norm(i["x"], 2 ** 20, act="silu", center=False)
+    pairs = i["x"].double().view(3, -1, 2)
+    v = (pairs / (pairs.square().mean(-1, keepdim=True) + 1e-5).sqrt()).view(3, -1)
+    want = v * torch.sigmoid(v)
+    # sums of 2 squares, 1 / sqrt, two products, silu of values below 1.5: under 24 roundings of 2^-24
+    assert ((got.double() - want).abs() <= 24 * 2.0 ** -24 * want.abs() + 1e-30).all()

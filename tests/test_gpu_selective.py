@@ -498,3 +498,39 @@ def test_extreme_rates_and_infinite_inputs(path):
             free = [k for k in range(n) if k != 5]
             assert torch.equal(got[1][free], c["init"][0][1][free]), "a step size of zero changed a state"
             assert got[7, 5] == float("-inf")
+
+
+def test_offsets_past_32_bits():
+    """Slots and rows whose element offsets pass 2^31 (and byte offsets 2^32): a cache of 6.4 GB and rows 2^26
+    elements apart, the largest stride."""
+    d, n, s = 48, 16, 3
+    i = step_inputs(s, d, n, 1, BF, seed=60)
+    slots = 2 ** 31 // (d * n) + 40
+    cache = torch.empty(slots, d, n, device="cuda")
+    high = torch.tensor([slots - 1, slots - 7, slots - 9], dtype=torch.int32, device="cuda")
+    to = torch.tensor([slots - 2, slots - 30, 5], dtype=torch.int32, device="cuda")
+    state = i["cache"][:s].clone()
+    cache[high.long()] = state
+    y = ssd.selective_step(i["u"], i["dt"], i["A"], i["B"], i["C"], cache, high, to, dt_bias=i["dt_bias"], D=i["D"],
+                           z=i["z"])
+    small = torch.cat([state, torch.zeros_like(state)])
+    near = torch.arange(2 * s, dtype=torch.int32, device="cuda")
+    want = ssd.selective_step(i["u"], i["dt"], i["A"], i["B"], i["C"], small, near[:s], near[s:], dt_bias=i["dt_bias"],
+                              D=i["D"], z=i["z"])
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(cache[to.long()], small[s:])
+
+    # the scan: 40 rows of u, z and y 2^26 elements apart, and a checkpoint in the last slot of the cache
+    j = make([33, 7], d, n, 1, BF, seed=61)
+    y0, f0, _ = call(j, chunk=16)
+    far = torch.empty(40 * 2 ** 26, dtype=BF, device="cuda")
+    views = [far.as_strided((40, d), (2 ** 26, 1), k * 64) for k in range(3)]
+    views[0].copy_(j["u"])
+    views[1].copy_(j["z"])
+    k = {**j, "u": views[0], "z": views[1]}
+    dst = torch.tensor([-1, slots - 3, -1, slots - 4], dtype=torch.int32, device="cuda")
+    y1, f1, m = call(k, chunk=16, y=views[2], chunk_states=cache, chunk_state_dst=dst)
+    assert int(m.error_flag.item()) == 0
+    assert torch.equal(y1, y0) and torch.equal(f1, f0)
+    assert torch.equal(cache[slots - 4], f1[1])
+    del far, views, k, cache
