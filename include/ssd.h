@@ -399,7 +399,7 @@ ssd_status ssd_causal_conv1d_varlen(
  *                  ssd_export_chunk_states (state_elems = channels*dstate)
  *                  feeds chunk_state_dst.
  * Supported: any channels >= 1 (channels % ngroups == 0), dstate in
- * {16, 32, 64, 128, 256}. y and the state outputs must not overlap an input.
+ * {16, 32, 64, 128, 256}, up to 2^30 tokens. y and the state outputs must not overlap an input.
  * Precision: all arithmetic and the state in float32; y is rounded once (to
  * nearest even). Results do not depend on the chunk size or on timing.
  * Errors: SSD_ERR_NULL_ARG, SSD_ERR_SHAPE (sizes, strides, float32 buffers
@@ -451,7 +451,8 @@ ssd_status ssd_selective_step(
  *                  be another sequence's read slot.
  *  error_flag      int32 [1] or NULL: a slot >= num_slots sets
  *                  SSD_DATA_BAD_SLOT; that sequence is skipped entirely.
- * Arithmetic and rounding are those of ssd_causal_conv1d_varlen.
+ * Arithmetic and rounding are those of ssd_causal_conv1d_varlen. out must not
+ * overlap an input.
  * Errors: SSD_ERR_DTYPE, SSD_ERR_SHAPE, SSD_ERR_UNSUPPORTED, SSD_ERR_NULL_ARG,
  * SSD_ERR_HIP.
  */

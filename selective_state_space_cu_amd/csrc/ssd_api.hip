@@ -334,6 +334,7 @@ ssd_status ssd_selective_scan_varlen(const void *u, int64_t u_stride, const void
                                      const int32_t *chunk_state_dst, int32_t chunk_states_capacity, void *stream) {
     ssd_status st = check_meta(meta);
     if (st != SSD_OK) return st;
+    if (meta->total_tokens > (1 << 30)) return SSD_ERR_SHAPE;   // token counts stay in 32 bits past a segment's end
     ssd::SelectiveArgs a{};
     a.u = u; a.dt = dt; a.B = B; a.C = C; a.z = z; a.dt_bias = dt_bias; a.A = A; a.D = D; a.y = y;
     a.u_stride = u_stride; a.dt_stride = dt_stride; a.B_stride = B_stride; a.C_stride = C_stride;

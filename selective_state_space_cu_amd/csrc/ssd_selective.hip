@@ -117,6 +117,15 @@ __device__ __forceinline__ float sum_scatter4(const float (&y)[4]) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// The slot that receives the state after a chunk (-1: none, also for a chunk that is not in the grid).
+__device__ __forceinline__ int chunk_slot(const SelectiveArgs &a, int chunk, bool report) {
+    if (chunk < 0 || chunk >= a.max_chunks) return -1;
+    const int slot = a.chunk_state_dst != nullptr ? a.chunk_state_dst[chunk] : chunk;
+    if (slot < a.capacity) return slot;
+    if (report) atomicOr(a.error_flag, SSD_DATA_BAD_SLOT);
+    return -1;
+}
+
 template <typename T, typename DT, int N>
 __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs a) {
     constexpr int NBLK = N / 16, SEG = kSeg, J = SEG / 4;
@@ -239,12 +248,7 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
         // the slot that receives the state after this segment, if a chunk ends here
         int slot = -1;
         if (a.chunk_states != nullptr && (!FULL || left == SEG || ((seg + 1) & (chunk_segs - 1)) == 0)) {
-            const int chunk = c0 + (seg >> chunk_shift);
-            slot = __builtin_amdgcn_readfirstlane(a.chunk_state_dst != nullptr ? a.chunk_state_dst[chunk] : chunk);
-            if (slot >= a.capacity) {
-                if (cb == 0 && lane == 0) atomicOr(a.error_flag, SSD_DATA_BAD_SLOT);
-                slot = -1;
-            }
+            slot = __builtin_amdgcn_readfirstlane(chunk_slot(a, c0 + (seg >> chunk_shift), cb == 0 && lane == 0));
         }
         float u[J];
         One z[J];
@@ -501,12 +505,8 @@ __global__ __launch_bounds__(64) void ssd_selective_walk_kernel(SelectiveArgs a)
         for (int k = 0; k < K; ++k)   // the sequence's last tokens
             if (t + k < end) token(k);
         if (a.chunk_states != nullptr) {
-            const int slot = a.chunk_state_dst != nullptr ? a.chunk_state_dst[chunk] : chunk;
-            if (slot >= a.capacity) {
-                if (cb == 0 && lane == 0) atomicOr(a.error_flag, SSD_DATA_BAD_SLOT);
-            } else if (slot >= 0) {
-                save(a.chunk_states + (int64_t)slot * a.C_total * N);
-            }
+            const int slot = chunk_slot(a, chunk, cb == 0 && lane == 0);
+            if (slot >= 0) save(a.chunk_states + (int64_t)slot * a.C_total * N);
         }
     }
     save(a.final_states + state_row);

@@ -507,6 +507,8 @@ def _rows(t: torch.Tensor, name: str, device, dtype, shape, row: int) -> int:
     apart, as a slice of a wider projection has them. Returns the elements from one row to the next."""
     if t.shape != shape or t.dtype != dtype or t.device != device:
         _refuse(t, name, device, dtype, shape)
+    if shape[0] > 0x7fffffff:
+        raise ValueError(f"{name} has {shape[0]} rows, more than 2^31 - 1")
     if t.is_contiguous():
         return row
     step = 1
@@ -572,6 +574,8 @@ def selective_scan_varlen(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B:
     device, f32 = u.device, torch.float32
     if u.shape[0] != meta.total_tokens:
         raise ValueError(f"u has {u.shape[0]} tokens, the metadata {meta.total_tokens}")
+    if meta.cu_seqlens.device != device:
+        raise ValueError(f"the metadata must be on {device}, got {meta.cu_seqlens.device}")
     states = (meta.nseqs, channels, n)
     cap = 0 if chunk_states is None else chunk_states.shape[0]
     init = _whole(initial_states, "initial_states", device, f32, states)
@@ -654,6 +658,8 @@ def group_norm(x: torch.Tensor, ngroups: int, weight: Optional[torch.Tensor] = N
         raise ValueError("z is given exactly with the gated forms")
     device, dtype, shape, f32 = x.device, x.dtype, x.shape, torch.float32
     channels = shape[1] if len(shape) == 2 else shape[1:].numel()
+    if not 0 < ngroups <= channels:
+        raise ValueError(f"ngroups must be between 1 and the {channels} channels, got {ngroups}")
     x_stride = _rows(x, "x", device, dtype, shape, channels)
     z_stride = 0 if z is None else _rows(z, "z", device, dtype, shape, channels)
     w = _whole(weight, "weight", device, f32, (channels,))

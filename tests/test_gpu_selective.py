@@ -223,6 +223,27 @@ def test_scan_checkpoints_through_the_plan_and_refuses_bad_slots():
     assert torch.equal(cache2[keep], cache[keep])
 
 
+@pytest.mark.parametrize("lengths,d", [([33, 20], 24), ([3, 5] * 32, 8192)], ids=["segments", "walk"])
+def test_scan_exports_no_chunk_outside_the_grid(lengths, d):
+    """Chunk numbers that the grid does not have (metadata of another batch) are never used as indices."""
+    i = make(lengths, d, 16, 1, BF, seed=14)
+    i["B"], i["C"] = i["B"].contiguous(), i["C"].contiguous()
+    meta = ssd.varlen_metadata(i["cu"], 16, total_tokens=sum(lengths))
+    meta.seq_chunk_start[0] = 10 ** 9
+    meta.seq_chunk_start[1] = -10 ** 6
+    dst = torch.arange(meta.max_chunks, dtype=torch.int32, device="cuda")
+    cst = torch.full((meta.max_chunks, d, 16), 7.0, device="cuda")
+    y, fin = ssd.selective_scan_varlen(i["u"], i["dt"], i["A"], i["B"], i["C"], meta, i["dt_bias"], i["D"], i["z"],
+                                       i["init"], i["has"], chunk_states=cst, chunk_state_dst=dst)
+    own = [int(c) for s, c in enumerate(meta.seq_chunk_start[:-1].tolist()) if s > 1]
+    rest = [c for c in range(meta.max_chunks) if c not in own]
+    assert int(meta.error_flag.item()) == 0
+    assert (cst[rest] == 7).all()
+    want = call(i, chunk=16)
+    assert torch.equal(y, want[0]) and torch.equal(fin, want[1])
+    assert torch.equal(cst[own], fin[2:])
+
+
 def test_scan_of_malformed_cu_seqlens_writes_nothing():
     i = make([20, 30], 16, 16, 1, F32, seed=12)
     i["cu"] = torch.tensor([0, 60, 50], dtype=torch.int32, device="cuda")
@@ -299,6 +320,13 @@ def test_step_in_place_fresh_and_unsaved_sequences():
     i["read"][1] = -1                # no state yet
     i["write"][2] = -1               # state not kept
     i["read"][3], i["write"][3] = -1, -1
+    before = i["cache"].clone()
+    check_step(i, before, step(i))
+
+
+def test_step_from_one_shared_slot():
+    i = step_inputs(5, 40, 16, 1, BF, seed=5)
+    i["read"][:] = i["read"][2].clone()   # branches of one sequence
     before = i["cache"].clone()
     check_step(i, before, step(i))
 

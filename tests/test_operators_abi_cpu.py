@@ -51,6 +51,7 @@ def test_scan_rejects_bad_meta_and_takes_an_empty_batch():
     assert _scan(m=_meta(null_field="seq_order")) == NULL
     assert _scan(m=_meta(cs=48)) == CHUNK
     assert _scan(m=_meta(max_chunks=1)) == CAPACITY
+    assert _scan(m=_meta(T=2 ** 30 + 1, max_chunks=2 ** 30)) == SHAPE
     none = dict(u=None, dt=None, B=None, C=None, y=None, z=None, fin=None)
     assert _scan(m=_meta(S=0, T=0, max_chunks=0), **none) == 0
 
@@ -152,6 +153,9 @@ def test_bindings_refuse():
             scan(kw=kw, **over)
     with pytest.raises(ValueError, match="tokens"):
         scan(meta=ssd.VarlenMeta(2, 11, 16, 3, *([z(1, dt=i32)] * 7)))
+    away = torch.zeros(1, dtype=i32, device="meta")
+    with pytest.raises(ValueError, match="metadata must be on"):
+        scan(meta=ssd.VarlenMeta(2, 10, 16, 3, *([away] * 7)))
     step = (z(3, 32), z(3, 32), z(32, 16), z(3, 1, 16), z(3, 1, 16))
     slots = z(3, dt=i32)
     with pytest.raises(ValueError, match="state_cache must"):
@@ -176,3 +180,8 @@ def test_bindings_refuse():
         ssd.group_norm(z(3, 32), 2, act="gate_last")
     with pytest.raises(ValueError, match="out must"):
         ssd.group_norm(z(3, 32), 2, out=z(3, 31))
+    for groups in (0, -1, 33, 2 ** 32 + 1):
+        with pytest.raises(ValueError, match="ngroups must"):
+            ssd.group_norm(z(3, 32), groups)
+    with pytest.raises(ValueError, match="more than"):
+        ssd.group_norm(torch.empty(2 ** 31, 1, dtype=torch.bfloat16, device="meta"), 1)
