@@ -67,12 +67,16 @@ template <typename T> __device__ __forceinline__ float load_f(const void *p, int
 // What bounds it: instruction issue. Per token and 16 channels x 16 states a wave
 // issues 4 exponentials (3.4 ns of a SIMD each), 20 products and sums (about 1 ns
 // with vector operands and an even number of waves) and its share of the rest, 56
-// ns in all; 80 are measured (4 x 8894 tokens, 4096 channels: 712 us, 1.7 TB/s),
-// the difference being LDS (half of its time taken) and waits.
+// ns in all; 79 are measured (4 x 8894 tokens, 4096 channels: 703 us, 1.7 TB/s).
+// Counters of that call: the vector unit is taken all the time, by 316
+// instructions a segment and wave (and 70 scalar, 43 LDS, 9 memory ones); LDS 44 %
+// of the time, without bank conflicts.
 // Tried and slower: b_t as an outer product on v_mfma_f32_4x4x1 (it holds the
 // vector unit for 5 ns and saves 4 products), 64 channels to a wave with B and C as
 // scalar operands (each such product takes twice as long), 16 tokens to a segment
-// or 5 waves a SIMD (the decays no longer fit the registers).
+// or 5 waves a SIMD (the decays no longer fit the registers), token after token with
+// 8 lanes to a channel and two states a lane (15 % fewer instructions, but 4 x 8894
+// tokens give it two waves a SIMD, too few to hide what each waits for: 929 us).
 constexpr int kSeg = 8;    // tokens of a segment
 constexpr int kCh = 16;    // channels of a workgroup
 
