@@ -68,9 +68,11 @@ template <typename T> __device__ __forceinline__ float load_f(const void *p, int
 // issues 4 exponentials (3.4 ns of a SIMD each), 20 products and sums (about 1 ns
 // with vector operands and an even number of waves) and its share of the rest, 56
 // ns in all; 79 are measured (4 x 8894 tokens, 4096 channels: 703 us, 1.7 TB/s).
-// Counters of that call: the vector unit is taken all the time, by 316
-// instructions a segment and wave (and 70 scalar, 43 LDS, 9 memory ones); LDS 44 %
-// of the time, without bank conflicts.
+// Counters of that call: 316 vector instructions a segment and wave (70 scalar, 43
+// LDS, 9 memory ones), 0.22 a cycle and SIMD with one exponential in eight; loops of
+// nothing else reach 0.26 (one in five) and 0.40 (none) with as many waves. Of 3.4
+// waves a SIMD 1.0 waits for LDS, memory or the chain. LDS is taken 44 % of the
+// time, without bank conflicts.
 // Tried and slower: b_t as an outer product on v_mfma_f32_4x4x1 (it holds the
 // vector unit for 5 ns and saves 4 products), 64 channels to a wave with B and C as
 // scalar operands (each such product takes twice as long), 16 tokens to a segment
