@@ -156,6 +156,11 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
     const int L = (int)(te - tb), c0 = a.seq_chunk_start[s];
     if (L <= a.walk_to) return;   // the walk's
     const int nseg = (L + SEG - 1) / SEG, nw = (int)blockDim.x >> 6;
+    // Waves of the workgroups of a CU are served oldest first, so one workgroup ran ahead of the others and the last was
+    // left alone on its CU. Priorities by what is left to do, in thirds of the longest sequence, keep them together (4 x
+    // 8894 tokens, 4096 channels, 4 workgroups of 4 waves on every CU: 737 us without, 672 with).
+    const int longest = a.seq_order[0];
+    const int third = longest < 0 || longest >= a.S ? nseg : (a.cu_seqlens[longest + 1] - a.cu_seqlens[longest]) / (3 * SEG);
     const int chunk_segs = a.cs / SEG, chunk_shift = __builtin_ctz(chunk_segs);
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -330,7 +335,7 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
 #pragma unroll
             for (int t = 0; t < SEG; ++t) asm volatile("" : "+v"(dec[t]), "+v"(inp[t]));   // before the wait, not after it
             asm volatile("" : "+v"(p), "+v"(h));
-            __builtin_amdgcn_s_setprio(2);     // the other waves wait for what follows
+            __builtin_amdgcn_s_setprio(3);     // the other waves wait for what follows
 
             // the chain: segment seg's wave is the only one that touches the buffer between done = seg and seg + 1.
             // LDS operations of a wave take effect in order: a state read after a counter that says so is that state
@@ -349,7 +354,9 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
             *state = h;
             asm volatile("" ::: "memory");
             if (lane == 0) done[nb] = seg + 1;
-            __builtin_amdgcn_s_setprio(0);
+            if (nseg - seg > 2 * third) __builtin_amdgcn_s_setprio(2);
+            else if (nseg - seg > third) __builtin_amdgcn_s_setprio(1);
+            else __builtin_amdgcn_s_setprio(0);
             asm volatile("" ::: "memory");
             if (slot >= 0) {
                 float *to = a.chunk_states + (int64_t)slot * a.C_total * N + nb * 16;   // uniform
@@ -585,10 +592,11 @@ __global__ __launch_bounds__(kSelStepThreads) void ssd_selective_step_kernel(Sel
 
 // Waves of a workgroup that splits sequences into segments: the fewer (sequence,
 // 16 channels) pairs there are, the more. Microseconds with 2 / 4 / 8 / 16 waves:
-// 16384 pairs (64 x 300 tokens) 375 / 395; 2560 (8 ragged prompts) 424 / 376 /
-// 392 / 448; 1024 (4 x 8894 tokens) 823 / 737 / 712 / 752; 160 (one prompt of
-// 30001 tokens) 2069 / 987 / 633 / 541.
-static int segment_waves(int64_t pairs) { return pairs >= 8192 ? 2 : pairs >= 2048 ? 4 : pairs >= 512 ? 8 : 16; }
+// 16384 pairs (64 x 300 tokens) 390 / 395; 8192 (32 x 500) 324 / 320; 2560 (8 ragged
+// prompts) 405 / 369 / 392 / 435; 1024 (4 x 4000) 362 / 300 / 320 / 346; 800 (5 x
+// 4000) 355 / 272 / 278 / 309; 512 (2 x 8000) 670 / 359 / 320 / 350; 320 (1 x 8000)
+// 670 / 335 / 269 / 295; 256 (1 x 8000) 564 / 273 / 197 / 184.
+static int segment_waves(int64_t pairs) { return pairs >= 16384 ? 2 : pairs >= 768 ? 4 : pairs > 256 ? 8 : 16; }
 
 // From this many (sequence, 64 channels) pairs on, 4 for every SIMD, sequences
 // are walked (64 prompts of 3 to 490 tokens, 8192 channels, 8192 pairs: 665 us in
