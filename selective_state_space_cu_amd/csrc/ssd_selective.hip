@@ -67,11 +67,11 @@ template <typename T> __device__ __forceinline__ float load_f(const void *p, int
 // What bounds it: instruction issue. Per token and 16 channels x 16 states a wave
 // issues 4 exponentials (3.4 ns of a SIMD each), 20 products and sums (about 1 ns
 // with vector operands and an even number of waves) and its share of the rest, 56
-// ns in all; 79 are measured (4 x 8894 tokens, 4096 channels: 703 us, 1.7 TB/s).
-// Counters of that call: 316 vector instructions a segment and wave (70 scalar, 43
-// LDS, 9 memory ones), 0.22 a cycle and SIMD with one exponential in eight; loops of
+// ns in all; 75 are measured (4 x 8894 tokens, 4096 channels: 668 us, 1.8 TB/s).
+// Counters of that call: 309 vector instructions a segment and wave (60 scalar, 32
+// LDS, 9 memory ones), 0.24 a cycle and SIMD with one exponential in eight; loops of
 // nothing else reach 0.26 (one in five) and 0.40 (none) with as many waves. Of 3.4
-// waves a SIMD 1.0 waits for LDS, memory or the chain. LDS is taken 44 % of the
+// waves a SIMD 0.7 waits for LDS, memory or the chain. LDS is taken 38 % of the
 // time, without bank conflicts.
 // Tried and slower: b_t as an outer product on v_mfma_f32_4x4x1 (it holds the
 // vector unit for 5 ns and saves 4 products), 64 channels to a wave with B and C as
