@@ -9,9 +9,11 @@
 // apart; a team goes on to the same group of other rows, so its weights are
 // loaded once. V is the widest of 16 bytes, 4 bytes and one value that the
 // group's size and all row starts are multiples of (16-byte accesses at odd
-// 4-byte places took 325 us where single values take 153: 16085 x 5055 float32
-// in groups of 337). That is 4.2 TB/s, and 35576 x 4096 bf16 with a gate in
-// groups of 1024 take 174 us, 5.0 TB/s, a large copy's rate.
+// 4-byte places took twice the time of single values). 16085 x 5055 float32 in
+// groups of 337 take 138 us, 4.7 TB/s, and 35576 x 4096 bf16 with a gate in groups
+// of 1024 170 us, 5.1 TB/s, a large copy's rate.
+#include <algorithm>
+
 #include "ssd_scan.hpp"
 
 namespace ssd {
@@ -104,7 +106,7 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void ssd_group_norm_kernel
         }
     const float inv = 1.0f / (float)size;
     for (int64_t row = row0; row < a.rows; row += rows_step) {
-        // (loading the next row here while this one is computed: 211 us instead of 153 for groups of 337 float32, the
+        // (loading the next row here while this one is computed took 1.4 times as long for groups of 337 float32: the
         // registers cost waves)
         const T *x = reinterpret_cast<const T *>(a.x) + row * a.x_stride + c0 + lane * V;
         const T *z = reinterpret_cast<const T *>(a.z) + row * a.z_stride + c0 + lane * V;
@@ -164,12 +166,23 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void ssd_group_norm_kernel
     }
 }
 
-constexpr int64_t kNormBlocks = 2048;   // workgroups of 256 threads that fill the card (8 a CU; one for every row and
-                                        // group instead: 281 us instead of 174 for 35576 x 4096 bf16 in 4 groups)
+// Workgroups of a launch: one round of what the CUs hold at once (a second, partial round costs as much as a full one: 8 a CU
+// instead took 154 us for 138 with groups of 337 float32, 388 for 294 in bf16), and of those only as many as have 48 KB of
+// inputs on their way in each CU (32 / 48 / 64 KB: 183 / 170 / 178 us for 35576 x 4096 bf16 with a gate in groups of 1024,
+// 141 / 136 / 135 for 20011 x 5120 in groups of 640). The runtime says 7 for kernels of few registers, but 7 a CU take
+// 168 us where 6 take 138.
+constexpr int64_t kNormCus = 256, kNormBytesAhead = 48 * 1024;
+constexpr int kNormMost = 6;
 
 template <typename T, int TEAM, int V, int R> static hipError_t launch_norm_team(const NormArgs &a, hipStream_t stream) {
     constexpr int THREADS = TEAM > 256 ? TEAM : 256, TEAMS = THREADS / TEAM;
-    const int64_t most = kNormBlocks * 256 / THREADS;
+    static const int resident = [] {
+        int n = 0;
+        const hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, ssd_group_norm_kernel<T, TEAM, V, R>, THREADS, 0);
+        return e == hipSuccess && n > 0 ? std::min(n, kNormMost) : 1;
+    }();
+    const int64_t bytes = (int64_t)TEAMS * a.size * sizeof(T) * (a.z != nullptr ? 2 : 1);   // of a workgroup's inputs at a time
+    const int64_t most = kNormCus * std::min<int64_t>(resident, (kNormBytesAhead + bytes - 1) / bytes);
     const int64_t need = ((int64_t)a.rows * a.groups + TEAMS - 1) / TEAMS;   // one team for every (row, group)
     int64_t blocks = need < most ? need : most;
     if (blocks * TEAMS < a.groups) blocks = (a.groups + TEAMS - 1) / TEAMS;
@@ -177,8 +190,8 @@ template <typename T, int TEAM, int V, int R> static hipError_t launch_norm_team
     return hipGetLastError();
 }
 
-// The smallest team that holds a group with 16 values a lane (8 where they are moved one by one: 153 us against 178 for
-// groups of 337 float32; 16 in the largest team).
+// The smallest team that holds a group with 16 values a lane (8 where they are moved one by one, which leaves more
+// waves: 14 % less time for groups of 337 float32; 16 in the largest team).
 template <typename T, int V, int TEAM = 1> static hipError_t launch_norm_size(const NormArgs &a, hipStream_t stream) {
     if constexpr (TEAM < 1024) {
         constexpr int R = V == 1 ? 8 : 16 / V;
