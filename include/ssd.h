@@ -401,7 +401,9 @@ ssd_status ssd_causal_conv1d_varlen(
  * Supported: any channels >= 1 (channels % ngroups == 0), dstate in
  * {16, 32, 64, 128, 256}, up to 2^30 tokens. y and the state outputs must not overlap an input.
  * Precision: all arithmetic and the state in float32; y is rounded once (to
- * nearest even). Results do not depend on the chunk size or on timing.
+ * nearest even). A decay below 2^-126 counts as 0; infinite states and rates
+ * A above 0 give what the recurrence gives token by token. Results do not
+ * depend on the chunk size or on timing.
  * Errors: SSD_ERR_NULL_ARG, SSD_ERR_SHAPE (sizes, strides, float32 buffers
  * not 16-byte aligned, other buffers not aligned to their element),
  * SSD_ERR_DTYPE, SSD_ERR_UNSUPPORTED (dstate), SSD_ERR_CHUNK_SIZE,

@@ -123,6 +123,11 @@ __device__ __forceinline__ float sum_scatter4(const float (&y)[4]) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// Whether some lane of the wave has a rate above 0.
+__device__ __forceinline__ bool any_above_zero(const f32x4 &r) {
+    return __any(fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3])) > 0.0f);
+}
+
 // The slot that receives the state after a chunk (-1: none, also for a chunk that is not in the grid).
 __device__ __forceinline__ int chunk_slot(const SelectiveArgs &a, int chunk, bool report) {
     if (chunk < 0 || chunk >= a.max_chunks) return -1;
@@ -171,7 +176,8 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
 
     float *carry = lds;                                           // [NBLK][64][4]
     lds_counter *done = (lds_counter *)(__attribute__((address_space(3))) int *)(lds + NBLK * 256);   // [NBLK] segments finished
-    float *mine = lds + NBLK * 256 + ((NBLK + 3) & ~3) + wave * (SEG * 64);
+    lds_counter *rising = done + NBLK;                                    // [NBLK] whether some rate is above 0
+    float *mine = lds + NBLK * 256 + ((2 * NBLK + 3) & ~3) + wave * (SEG * 64);
     float *ldsD = mine;                 // [SEG tokens][16 channels] (delta log2 e, delta u)
     float *ldsB = mine + SEG * 32;      // [SEG tokens][16 states]
     float *ldsC = mine + SEG * 48;
@@ -181,7 +187,7 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
     // What is needed once a segment or less often is worked out anew from the lane's number, which the compiler is kept
     // from knowing: kept over the segments, it pushes other values out to scratch memory inside the loops. state_col is the
     // lane's place in a state. (One block of states leaves room for d; without it nothing goes to scratch memory at all, but
-    // 30001 bf16 tokens of 2560 channels take 560 us for 545, 4 float32 prompts of 4096 channels 167 for 152.)
+    // 30001 bf16 tokens of 2560 channels take 568 us for 549, 4 float32 prompts of 4096 channels 161 for 151.)
     auto anew = [&] {
         int here = lane;
         asm volatile("" : "+v"(here));
@@ -202,10 +208,15 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
         const f32x4 h = start ? *reinterpret_cast<const f32x4 *>(a.init + state_row + nb * 16 + state_col()) : f32x4{0, 0, 0, 0};
         *reinterpret_cast<f32x4 *>(carry + (nb * 64 + lane) * 4) = h;
         if (nseg == 0) *reinterpret_cast<f32x4 *>(final + nb * 16 + state_col()) = h;
-        if (lane == 0) done[nb] = 0;
+        const bool up = any_above_zero(*reinterpret_cast<const f32x4 *>(a.A + nb * 16 + state_col()));
+        if (lane == 0) {
+            done[nb] = 0;
+            rising[nb] = up;
+        }
     }
     __syncthreads();
     if (wave >= nseg) return;
+    const bool growing = __any(lane < NBLK && rising[lane < NBLK ? lane : 0] != 0);
 
     const float bias = a.dt_bias != nullptr ? a.dt_bias[d] : 0.0f, skip = a.D != nullptr ? a.D[d] : 0.0f;
     f32x4 rate = *reinterpret_cast<const f32x4 *>(a.A + (int64_t)d * N + 4 * q);
@@ -351,6 +362,8 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
 #pragma unroll
             for (int t = 0; t < SEG; ++t) asm volatile("" : "+v"(dec[t]), "+v"(inp[t]));   // before the wait, not after it
             asm volatile("" : "+v"(p), "+v"(h));
+            // Whether a lane's decays may have a product outside float32's range.
+            const bool doubtful = growing || __any(fminf(fminf(p[0], p[1]), fminf(p[2], p[3])) == 0.0f);
             __builtin_amdgcn_s_setprio(3);     // the other waves wait for what follows
 
             // the chain: segment seg's wave is the only one that touches the buffer between done = seg and seg + 1.
@@ -367,6 +380,20 @@ __global__ __launch_bounds__(1024) void ssd_selective_scan_kernel(SelectiveArgs 
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) h[i] = fmaf(p[i], in[i], h[i]);
+            // Such a product times the state is not the decays one by one: 0 times an infinite state is NaN where each decay
+            // leaves it infinite, infinity times a small one is not finite. So states that are not go token by token.
+            if (doubtful) {
+                const float sum = (h[0] + h[1]) + (h[2] + h[3]);
+                if (__builtin_expect(__any(!(fabsf(sum) < __builtin_inff())), 0)) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v = in[i];
+#pragma unroll
+                        for (int t = 0; t < SEG; ++t) v = fmaf(dec[t][i], v, inp[t][i]);
+                        if (!(fabsf(h[i]) < __builtin_inff())) h[i] = v;
+                    }
+                }
+            }
             *state = h;
             asm volatile("" ::: "memory");
             if (lane == 0) done[nb] = seg + 1;
@@ -637,7 +664,7 @@ template <typename T, typename DT, int N> struct SelectiveLaunch {
         const int waves = segment_waves(blocks);
         if (!fits_grid(blocks, 64 * waves)) return hipErrorInvalidConfiguration;
         constexpr int NBLK = N / 16;
-        const size_t lds = sizeof(float) * (NBLK * 256 + ((NBLK + 3) & ~3) + (size_t)waves * kSeg * 64);
+        const size_t lds = sizeof(float) * (NBLK * 256 + ((2 * NBLK + 3) & ~3) + (size_t)waves * kSeg * 64);
         hipLaunchKernelGGL((ssd_selective_scan_kernel<T, DT, N>), dim3((unsigned)blocks), dim3(64 * waves), lds,
                            stream, a);
         return hipGetLastError();
