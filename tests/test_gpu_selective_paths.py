@@ -6,8 +6,9 @@ import torch
 
 import selective_bound as bound
 import selective_ref as ref
+from gpu_util import log
 from selective_state_space_cu_amd import ssd
-from test_gpu_selective import BF, F32, call, cpu, make, starts
+from test_gpu_selective import BF, F32, call, cpu, make, starts, step, step_inputs
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
@@ -95,3 +96,151 @@ def test_vanishing_decays_of_large_states(form):
         ry, rh, by, bh, r = one_sequence(c, k)
         ref.check(fin[k], rh[-1], bh[-1], f"state {k}")
         ref.check(y[r], ry, by, f"y {k}")
+
+
+def check_sequences(i, y, fin, cst, chunk, sequences):
+    """y, final and exported states of some sequences of a batch; returns the worst part of the bound."""
+    c, worst = cpu(i), 0.0
+    first = [0]
+    for v in i["lengths"]:
+        first.append(first[-1] + -(-v // chunk))
+    for s in sequences:
+        ry, rh, by, bh, r = one_sequence(c, s)
+        n = i["lengths"][s]
+        if n == 0:
+            start = starts(c, s)
+            assert torch.equal(fin[s].cpu(), torch.zeros_like(fin[s].cpu()) if start is None else start), f"empty {s}"
+            continue
+        worst = max(worst, ref.check(y[r], ry, by, f"y of {s}"), ref.check(fin[s], rh[-1], bh[-1], f"state of {s}"))
+        for k in range(-(-n // chunk) if cst is not None else 0):
+            last = min(chunk * (k + 1), n) - 1
+            worst = max(worst, ref.check(cst[first[s] + k], rh[last], bh[last], f"chunk {k} of {s}"))
+    return worst
+
+
+SMALL = [
+    # lengths, channels, states, groups, type, type of dt, gate, initial states: 16 waves of segments
+    ([1], 16, 16, 1, BF, None, True, "none"), ([17, 64, 47], 64, 16, 1, F32, None, True, "even"),
+    ([15, 0, 1, 33, 0], 100, 16, 2, BF, F32, True, "even"), ([129, 70], 24, 32, 3, F32, BF, True, "all"),
+    ([300, 19], 72, 64, 2, BF, None, True, "all"), ([65, 31], 10, 128, 1, F32, None, False, "even"),
+    ([90, 50], 18, 256, 1, BF, None, True, "all"), ([1037, 3], 31, 16, 1, F32, None, True, "even"),
+]
+
+
+@pytest.mark.parametrize("k", range(len(SMALL)))
+def test_sixteen_waves(k):
+    lengths, d, n, g, dtype, dt_dtype, gate, init = SMALL[k]
+    log(f"segments {SMALL[k]}")
+    i = make(lengths, d, n, g, dtype, dt_dtype, gate, init, seed=100 + k)
+    meta = ssd.varlen_metadata(i["cu"], 16, total_tokens=sum(lengths))
+    cst = torch.full((meta.max_chunks, d, n), float("nan"), device="cuda")
+    y, fin, meta = call(i, chunk=16, chunk_states=cst)
+    assert int(meta.error_flag.item()) == 0
+    log(f"  worst {check_sequences(i, y, fin, cst, 16, range(len(lengths))):.3f} of the bound")
+
+
+# A workgroup of segments has 2, 4 or 8 waves by the number of (sequence, 16 channels) pairs; each of its waves takes
+# several segments here, and sequences end in whole and in partial ones.
+WAVES = [
+    # waves, sequences, tokens of the longest, channels, states, groups, type, gate, initial states
+    (8, 9, 210, 520, 16, 1, BF, True, "even"), (8, 12, 150, 400, 64, 2, F32, False, "all"),
+    (8, 260, 140, 12, 32, 1, BF, True, "even"), (8, 9, 140, 530, 256, 1, F32, True, "all"),
+    (4, 24, 120, 520, 16, 1, F32, True, "even"), (4, 50, 90, 264, 128, 8, BF, True, "none"),
+    (4, 200, 70, 90, 32, 3, F32, False, "even"), (2, 500, 70, 528, 64, 1, BF, True, "even"),
+    (2, 1030, 60, 250, 64, 2, F32, False, "all"), (2, 300, 50, 1030, 16, 1, BF, True, "even"),
+]
+
+
+@pytest.mark.parametrize("k", range(len(WAVES)))
+def test_two_to_eight_waves(k):
+    waves, s, longest, d, n, g, dtype, gate, init = WAVES[k]
+    log(f"segments {WAVES[k]}")
+    pairs = s * g * -(-(d // g) // 16)
+    assert {8: 256 < pairs < 768, 4: 768 <= pairs < 16384, 2: pairs >= 16384}[waves], pairs
+    # (16 and 32 states: rows of B and C off 4-byte boundaries, or too few pairs, so that nothing is walked)
+    lengths = torch.randint(0, longest + 1, (s,), generator=torch.Generator().manual_seed(k)).tolist()
+    lengths[:6] = [longest, 16 * waves, 8 * waves + 3, 0, 1, 8]
+    i = make(lengths, d, n, g, dtype, None, gate, init, seed=120 + k)
+    meta = ssd.varlen_metadata(i["cu"], 32, total_tokens=sum(lengths))
+    cst = torch.full((meta.max_chunks, d, n), float("nan"), device="cuda")
+    y, fin, meta = call(i, chunk=32, chunk_states=cst)
+    assert int(meta.error_flag.item()) == 0
+    assert torch.isfinite(fin).all() and torch.isfinite(y).all()
+    used = sum(-(-v // 32) for v in lengths)
+    assert torch.isfinite(cst[:used]).all() and torch.isnan(cst[used:]).all()
+    log(f"  worst {check_sequences(i, y, fin, cst, 32, [0, 1, 2, 3, 4, 5, s // 2, s - 1]):.3f} of the bound")
+
+
+@pytest.mark.parametrize("n,dtype,dt_dtype,gate,g", [(16, BF, F32, True, 1), (32, F32, None, False, 2)])
+def test_walk(n, dtype, dt_dtype, gate, g):
+    """4096 and more pairs; a sequence more than 3 times the mean goes in segments beside the walk."""
+    r = torch.Generator().manual_seed(n)
+    lengths = torch.randint(0, 45, (258,), generator=r).tolist()
+    lengths[:6] = [400, 64, 33, 0, 1, 2]
+    i = make(lengths, 1044, n, g, dtype, dt_dtype, gate, "even", seed=140 + n)
+    on_words(i, n)
+    meta = ssd.varlen_metadata(i["cu"], 32, total_tokens=sum(lengths))
+    cst = torch.full((meta.max_chunks, 1044, n), float("nan"), device="cuda")
+    y, fin, meta = call(i, chunk=32, chunk_states=cst)
+    assert int(meta.error_flag.item()) == 0
+    assert torch.isfinite(fin).all() and torch.isfinite(y).all()
+    log(f"  worst {check_sequences(i, y, fin, cst, 32, [0, 1, 2, 3, 4, 5, 129, 257]):.3f} of the bound")
+
+
+# A step takes two sequences to a workgroup from 2048 workgroups on (channels of a workgroup: 1024 / states).
+STEPS = [
+    # sequences, channels, states, groups, type, type of dt, gate
+    (257, 1040, 16, 1, BF, None, True), (301, 1752, 32, 3, F32, BF, False), (121, 1100, 128, 2, BF, F32, True),
+    (4097, 70, 16, 1, F32, None, True), (65, 1008, 256, 1, BF, None, True),
+]
+
+
+@pytest.mark.parametrize("k", range(len(STEPS)))
+def test_step_of_two_sequences_a_workgroup(k):
+    """An odd number of sequences, with fresh, unsaved, in-place and refused ones in both places of a pair."""
+    s, d, n, g, dtype, dt_dtype, gate = STEPS[k]
+    log(f"step {STEPS[k]}")
+    assert -(-s // 2) * -(-d // (1024 // n)) >= 2048
+    i = step_inputs(s, d, n, g, dtype, dt_dtype, gate, seed=160 + k)
+    slots = i["cache"].shape[0]
+    for at in (4, 7):                     # first and second of a pair, and the same again where the last one stands alone
+        i["read"][at] = -1
+        i["write"][at + 4] = -1
+        i["write"][at + 8] = i["read"][at + 8].clone()
+        i["read"][at + 12] = slots
+        i["write"][at + 16] = slots + 5
+    i["read"][-1] = slots + 1
+    refused = [16, 19, 20, 23, s - 1]
+    before = i["cache"].clone()
+    y = torch.full((s, d), 3.0, dtype=dtype, device="cuda")
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    step(i, y=y, error_flag=flag)
+    assert int(flag.item()) == ssd.DATA_BAD_SLOT
+    assert (y[refused] == 3).all()
+    c, old, new = cpu(i), before.cpu(), i["cache"].cpu()
+    written = set()
+    for q in range(s):
+        rs, ws = int(c["read"][q]), int(c["write"][q])
+        if q in refused:
+            continue
+        r = slice(q, q + 1)
+        if q < 30 or q % 16 == 1 or q > s - 4:
+            ry, rh, by, bh = bound.scan(c["u"][r], c["dt"][r], c["A"], c["B"][r], c["C"][r], c["dt_bias"], c["D"],
+                                        None if c["z"] is None else c["z"][r], old[rs] if rs >= 0 else None)
+            ref.check(y[r], ry, by, f"y of {q}")
+            if ws >= 0:
+                ref.check(new[ws], rh[-1], bh[-1], f"state of {q}")
+        written.add(ws)
+    kept = [v for v in range(slots) if v not in written]
+    assert torch.equal(new[kept], old[kept]), "a slot that no sequence writes was written"
+    assert torch.isfinite(new).all() and torch.isfinite(y).all()
+    # alone, one sequence a workgroup: the same bits
+    some = [0, 1, 4, 8, 12, s - 2]
+    pick = torch.tensor(some, device="cuda")
+    j = {**i, **{name: None if i[name] is None else i[name][pick] for name in ("u", "dt", "B", "C", "z")},
+         "cache": before.clone(), "read": i["read"][pick], "write": i["write"][pick]}
+    assert torch.equal(step(j), y[pick])
+    for q in some:
+        ws = int(c["write"][q])
+        if ws >= 0:
+            assert torch.equal(j["cache"][ws], i["cache"][ws]), f"state of {q}"
