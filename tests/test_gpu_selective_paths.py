@@ -244,3 +244,48 @@ def test_step_of_two_sequences_a_workgroup(k):
         ws = int(c["write"][q])
         if ws >= 0:
             assert torch.equal(j["cache"][ws], i["cache"][ws]), f"state of {q}"
+
+
+@pytest.mark.parametrize("s,d", [(5, 48), (260, 1040)], ids=["segments", "walk"])
+def test_graph_of_metadata_and_scan_replays_with_other_lengths(s, d):
+    """The same number of sequences and tokens, cut elsewhere before every replay (a long one among short ones, empty
+    ones): what is chosen on the host holds for any cut."""
+    total = 20 * s
+    i = make([20] * s, d, 16, 1, BF, init="all", seed=180)
+    on_words(i, 16)
+    y = torch.empty_like(i["u"])
+    fin = torch.empty(s, d, 16, device="cuda")
+    cu = i["cu"].clone()
+
+    def both():
+        meta = ssd.varlen_metadata(cu, 16, total_tokens=total)
+        ssd.selective_scan_varlen(i["u"], i["dt"], i["A"], i["B"], i["C"], meta, dt_bias=i["dt_bias"], D=i["D"], z=i["z"],
+                                  initial_states=i["init"], y=y, final_states=fin)
+        return meta
+    with torch.cuda.stream(torch.cuda.Stream()):
+        both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    r = torch.Generator().manual_seed(181)
+    for turn in range(4):
+        cuts = torch.randint(0, total + 1, (s - 1,), generator=r).sort().values
+        if turn == 1:
+            cuts[:] = 0                      # one sequence has all the tokens
+        if turn == 2:
+            cuts = torch.cat([cuts[:s // 2].clamp(max=total // 2).sort().values, torch.full((s - 1 - s // 2,), total)])
+        now = torch.cat([torch.tensor([0]), cuts, torch.tensor([total])]).to(torch.int32)
+        cu.copy_(now)
+        both()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (y, fin)]
+        y.fill_(-1.0)
+        fin.fill_(-1.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(fin, want[1]), f"replay {turn}"
+        lengths = (now[1:] - now[:-1]).tolist()
+        j = {**i, "lengths": lengths, "has": None}
+        longest = max(range(s), key=lambda k: lengths[k])
+        check_sequences(j, y, fin, None, 16, [longest] if lengths[longest] > 1500 else [longest, 0, s - 1])
