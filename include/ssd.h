@@ -403,7 +403,11 @@ ssd_status ssd_causal_conv1d_varlen(
  * Precision: all arithmetic and the state in float32; y is rounded once (to
  * nearest even). A decay below 2^-126 counts as 0; infinite states and rates
  * A above 0 give what the recurrence gives token by token. Results do not
- * depend on the chunk size or on timing.
+ * depend on the chunk size or on timing. A sequence's results may differ by
+ * float32 roundings with the batch around it (the number of sequences, their
+ * mean length) and with whether the rows of B and C lie on 4-byte boundaries:
+ * these choose whether it is taken token by token or in segments of 8 tokens,
+ * whose ends are joined in another order of sums.
  * Errors: SSD_ERR_NULL_ARG, SSD_ERR_SHAPE (sizes, strides, float32 buffers
  * not 16-byte aligned, other buffers not aligned to their element),
  * SSD_ERR_DTYPE, SSD_ERR_UNSUPPORTED (dstate), SSD_ERR_CHUNK_SIZE,

@@ -569,7 +569,8 @@ def selective_scan_varlen(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B:
     """ssd_selective_scan_varlen: the scan with a decay per channel and state. u, dt, z (T, D) and B, C (T, G, N)
     may be slices with rows further apart; A (D, N), dt_bias, D (D,) and the states (S, D, N) are float32.
     `chunk_states` (float32 [slots, D, N]) receives the state after each chunk, at index c or at
-    chunk_state_dst[c] when given. Returns (y, final_states)."""
+    chunk_state_dst[c] when given. Float32 roundings of a sequence's results may differ with the batch around it.
+    Returns (y, final_states)."""
     head, channels, n, groups = _selective_inputs(u, dt, A, B, C, dt_bias, D, z)
     device, f32 = u.device, torch.float32
     if u.shape[0] != meta.total_tokens:
