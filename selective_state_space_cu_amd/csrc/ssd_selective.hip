@@ -67,8 +67,8 @@ template <typename T> __device__ __forceinline__ float load_f(const void *p, int
 // What bounds it: instruction issue. Per token and 16 channels x 16 states a wave
 // issues 4 exponentials (3.4 ns of a SIMD each), 20 products and sums (about 1 ns
 // with vector operands and an even number of waves) and its share of the rest, 56
-// ns in all; 75 are measured (4 x 8894 tokens, 4096 channels: 668 us, 1.8 TB/s).
-// Counters of that call: 309 vector instructions a segment and wave (60 scalar, 32
+// ns in all; 75 are measured (4 x 8894 tokens, 4096 channels: 672 us, 1.8 TB/s).
+// Counters of that call: 314 vector instructions a segment and wave (64 scalar, 32
 // LDS, 9 memory ones), 0.24 a cycle and SIMD with one exponential in eight; loops of
 // nothing else reach 0.26 (one in five) and 0.40 (none) with as many waves. Of 3.4
 // waves a SIMD 0.7 waits for LDS, memory or the chain. LDS is taken 38 % of the
