@@ -59,7 +59,7 @@ typedef enum {
     SSD_ERR_NULL_ARG = 1,     /* a required pointer is NULL */
     SSD_ERR_CHUNK_SIZE = 2,   /* chunk_size not a power of two in [16, 256] */
     SSD_ERR_SHAPE = 3,        /* negative/zero sizes, nheads % ngroups != 0, ... */
-    SSD_ERR_BLOCK_SIZE = 4,   /* block_size <= 0 or not a multiple of chunk_size */
+    SSD_ERR_BLOCK_SIZE = 4,   /* block_size <= 0 or not a multiple of chunk_size (of 16 in a key-value cache) */
     SSD_ERR_CAPACITY = 5,     /* max_chunks < total_tokens/chunk_size + nseqs, or a too small output capacity */
     SSD_ERR_DTYPE = 6,        /* unknown ssd_dtype */
     SSD_ERR_HIP = 7,          /* a HIP launch or attribute call failed */
@@ -72,7 +72,8 @@ typedef enum { SSD_F32 = 0, SSD_BF16 = 1 } ssd_dtype;
 #define SSD_DATA_BAD_CU_SEQLENS 1   /* cu_seqlens[0] != 0, decreasing, or last != total_tokens */
 #define SSD_DATA_TOO_MANY_CHUNKS 2  /* sum of ceil(len/chunk_size) > max_chunks */
 #define SSD_DATA_BAD_SLOT 4         /* a cache slot >= its buffer's slot count */
-#define SSD_DATA_BAD_BLOCK 8        /* a touched block index >= max_blocks_per_seq */
+#define SSD_DATA_BAD_BLOCK 8        /* a touched block index >= max_blocks_per_seq, or a block outside its cache */
+#define SSD_DATA_NO_BLOCK 16        /* fewer free blocks than the new tokens need */
 
 /*
  * Varlen chunk metadata of one packed batch (built once, shared by all layers).
@@ -501,6 +502,263 @@ ssd_status ssd_group_norm(
     const void *x, int64_t x_stride, const void *z, int64_t z_stride, const float *weight, const float *bias,
     ssd_dtype in_dtype, int32_t rows, int32_t channels, int32_t ngroups, float eps, int32_t center,
     ssd_norm_act act, void *out, int64_t out_stride, void *stream);
+
+/*
+ * One decode step of the gated delta rule, with the dual state anchors of
+ * ssd_decode_step: the recurrent form of ssd_gated_delta_chunk_varlen (the
+ * fused recurrent and sigmoid-gating kernels that the prefix-caching page
+ * names, Purpose, kernels/layers item). Each sequence has one new token, or
+ * several (tokens speculated ahead, say: the state after each is kept, and the
+ * next step reads the slot of the last accepted one). Per value head h (key
+ * head g = h / (nheads/nkheads)), with the state S (dv x dk), token by token:
+ *     S    = state_cache[read_slot[s], h]          (zero when read_slot[s] < 0)
+ *     S    = e^(gate) S;  S += beta (v[t,h] - S k[t,g]) k[t,g]^T
+ *     o[t,h] = scale S q[t,g]
+ *     state_cache[write_slot[t], h] = S            (skipped when write_slot[t] < 0)
+ * A == NULL: gate and beta are the log-decay and the write strength, as in the
+ * chunk call. A != NULL: they are raw, and
+ *     gate = A[h] softplus(gate + dt_bias[h]),  beta = 1 / (1 + e^-beta).
+ * qk_eps >= 0: q and k are divided by sqrt(|q|^2 + qk_eps) first; qk_eps < 0:
+ * they are taken as they are.
+ *
+ *  q, k            element type `in_dtype`, (T, nkheads, dk)
+ *  v, o            element type `in_dtype`, (T, nheads, dv)
+ *  gate, beta      element type `gate_dtype`, (T, nheads)
+ *  *_stride        elements from one token's row to the next (rows themselves
+ *                  are contiguous): at least the row's length, at most 2^26
+ *  A, dt_bias      float32 (nheads); dt_bias may be NULL (= 0)
+ *  cu_seqlens      int32 (nseqs+1) on the device: sequence s has the tokens
+ *                  cu_seqlens[s] .. cu_seqlens[s+1]-1, any number of them; or
+ *                  NULL: one token each (total_tokens == nseqs)
+ *  state_cache     float32 (num_slots, nheads, dv, dk), 16-byte aligned,
+ *                  updated in place
+ *  read_slot       int32 (nseqs); write_slot int32 (total_tokens). A sequence
+ *                  may write the slot it reads. Otherwise write slots must be
+ *                  unique and must not be another sequence's read slot (else
+ *                  unspecified).
+ *  error_flag      int32 [1] or NULL: a slot >= num_slots sets
+ *                  SSD_DATA_BAD_SLOT, a sequence outside [0, total_tokens]
+ *                  SSD_DATA_BAD_CU_SEQLENS; that sequence is skipped entirely.
+ * Supported: dk in {64, 128, 256}, any dv >= 1, nheads % nkheads == 0. o must
+ * not overlap an input.
+ * Precision: all arithmetic and the state in float32; o is rounded once (to
+ * nearest even). Results do not depend on the batch around a sequence.
+ * Errors: SSD_ERR_DTYPE, SSD_ERR_SHAPE (sizes, strides, alignment of the cache
+ * or to the element, total_tokens != nseqs without cu_seqlens, a scale or
+ * qk_eps that is not a number), SSD_ERR_UNSUPPORTED (dk), SSD_ERR_NULL_ARG,
+ * SSD_ERR_HIP.
+ */
+ssd_status ssd_gated_delta_step(
+    const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+    const void *gate, int64_t gate_stride, const void *beta, int64_t beta_stride, const float *A,
+    const float *dt_bias, float qk_eps, float scale, ssd_dtype in_dtype, ssd_dtype gate_dtype, int32_t nseqs,
+    int32_t total_tokens, const int32_t *cu_seqlens, int32_t nheads, int32_t nkheads, int32_t dk, int32_t dv,
+    float *state_cache, int32_t num_slots, const int32_t *read_slot, const int32_t *write_slot, void *o,
+    int64_t o_stride, int32_t *error_flag, void *stream);
+
+/*
+ * Block tables and slot maps of one step, built on the device from the
+ * requests' lengths: what the calls of all layers share (the prefix-caching
+ * page builds block indices and anchors with the rest of the batch metadata).
+ * Request s has num_computed[s] tokens in the caches and num_new[s] >= 0 more
+ * in this step, packed in the order of the requests. Its blocks, of block_size
+ * tokens each, are the entries 0, 1, .. of row rows[s] (s when rows is NULL)
+ * of block_table.
+ *  1. The blocks that the new tokens begin,
+ *         ceil((computed + new) / block_size) - ceil(computed / block_size),
+ *     are taken from the end of free_blocks[0 .. *free_count), request by
+ *     request, and entered into block_table; *free_count_out is what is left.
+ *     free_blocks == NULL: the table already has them.
+ *  2. The maps are written (none may be NULL):
+ *  cu_seqlens      (nseqs+1) prefix sums of num_new
+ *  seq_lens        (nseqs) computed + new
+ *  positions       (total_tokens) position of the token in its request
+ *  token_seq       (total_tokens) its request
+ *  slots           (total_tokens) block * block_size + position % block_size
+ *                  of the position's block: where kv_cache_write puts it
+ *  read_slot       (nseqs) the block of the last computed token, or -1: the
+ *                  read anchor of a state cache with a slot per block
+ *  state_slot      (total_tokens) the position's block for a request's last
+ *                  token and for the last token of a block, else -1: the
+ *                  write_slot of ssd_gated_delta_step, which so keeps the state
+ *                  at every block's end and after the last token
+ * Tokens at and past cu_seqlens[nseqs] get -1 everywhere (a padded batch).
+ * A request is refused, with its bit set in error_flag, when its counts are
+ * negative, its num_new exceeds total_tokens or its length 2^31-1
+ * (SSD_DATA_BAD_CU_SEQLENS), its row is outside the table (SSD_DATA_BAD_SLOT),
+ * it has more blocks than the table's max_blocks columns (SSD_DATA_BAD_BLOCK),
+ * or the new blocks of the requests up to and with it, refused for lack of
+ * blocks or not, are more than *free_count and it needs some
+ * (SSD_DATA_NO_BLOCK). A refused request takes no block, its table row stays
+ * as it was, its tokens keep their place in the batch, and it gets seq_lens 0,
+ * read_slot -1 and -1 for its tokens' positions, slots and state slots. A block
+ * outside [0, num_blocks) that the table holds gives -1, flagged as
+ * SSD_DATA_BAD_BLOCK unless negative. More new tokens in all than total_tokens:
+ * SSD_DATA_BAD_CU_SEQLENS, the maps hold the first total_tokens.
+ *
+ *  num_computed, num_new  int32 (nseqs)
+ *  rows            int32 (nseqs), distinct, or NULL
+ *  block_table     int32 (table_rows, max_blocks), updated in place
+ *  free_blocks     int32 (num_free) or NULL; free_count int32 [1], at most
+ *                  num_free; free_count_out int32 [1], may be free_count itself
+ *                  (both may be NULL when free_blocks is NULL)
+ * All pointers are device pointers. One launch for up to 4096 tokens, two
+ * beyond. nseqs, total_tokens and max_blocks up to 2^20, num_free up to 2^29,
+ * num_blocks * block_size up to 2^31 - 1.
+ * Errors: SSD_ERR_NULL_ARG, SSD_ERR_SHAPE (sizes outside these),
+ * SSD_ERR_BLOCK_SIZE (block_size < 1), SSD_ERR_HIP.
+ */
+ssd_status ssd_step_tables(
+    int32_t nseqs, int32_t total_tokens, const int32_t *num_computed, const int32_t *num_new, const int32_t *rows,
+    int32_t *block_table, int32_t table_rows, int32_t max_blocks, int32_t block_size, int32_t num_blocks,
+    const int32_t *free_blocks, int32_t num_free, const int32_t *free_count, int32_t *free_count_out,
+    int32_t *cu_seqlens, int32_t *seq_lens, int32_t *positions, int32_t *token_seq, int32_t *slots,
+    int32_t *read_slot, int32_t *state_slot, int32_t *error_flag, void *stream);
+
+/*
+ * Write of new tokens' keys and values to a paged cache: token t goes to slot
+ * slots[t] = block * block_size + place (ssd_step_tables makes them), negative
+ * slots are skipped.
+ *     k_cache[block, h, place, :] = k[t, h, :]
+ *     v_cache[block, h, :, place] = v[t, h, :]
+ *  k, v            element type `dtype`, (total_tokens, nkvheads, head_dim), rows
+ *                  *_stride elements apart (at least the row, at most 2^26)
+ *  k_cache         `dtype`, (num_blocks, nkvheads, block_size, head_dim)
+ *  v_cache         `dtype`, (num_blocks, nkvheads, head_dim, block_size): the
+ *                  keys of a block side by side, so that the attention's second
+ *                  product takes them from memory as they lie
+ *                  (both 16-byte aligned)
+ *  slots           int32 (total_tokens) on the device; distinct where >= 0
+ *  error_flag      int32 [1] or NULL: a slot >= num_blocks * block_size sets
+ *                  SSD_DATA_BAD_SLOT and is skipped.
+ * Supported: head_dim in {64, 128, 256}, block_size a multiple of 16,
+ * num_blocks * block_size up to 2^31 - 1.
+ * Errors: SSD_ERR_DTYPE, SSD_ERR_SHAPE, SSD_ERR_BLOCK_SIZE, SSD_ERR_UNSUPPORTED
+ * (head_dim), SSD_ERR_NULL_ARG, SSD_ERR_HIP.
+ */
+ssd_status ssd_kv_cache_write(
+    const void *k, int64_t k_stride, const void *v, int64_t v_stride, ssd_dtype dtype, int32_t total_tokens,
+    int32_t nkvheads, int32_t head_dim, void *k_cache, void *v_cache, int32_t num_blocks, int32_t block_size,
+    const int32_t *slots, int32_t *error_flag, void *stream);
+
+/*
+ * How one step's attention over a paged cache is split, built once on the
+ * device and shared by the layers of a step that have the same window. The
+ * keys of every sequence fall into parts of part_keys keys; the parts of all
+ * sequences, numbered in order, are what the attention's workgroups take.
+ * The struct itself lives in host memory; its array fields are device buffers
+ * the caller owns.
+ */
+typedef struct {
+    int32_t nseqs;              /* [host] S >= 0 */
+    int32_t total_tokens;       /* [host] T: rows of q */
+    int32_t max_new_tokens;     /* [host] most tokens of a sequence, 1 .. 64 */
+    int32_t window;             /* [host] keys a token sees, its own among them; 0: all */
+    int32_t max_parts;          /* [host] capacity, > S; max_parts - S parts are aimed at */
+    const int32_t *seq_lens;    /* in  [S] keys of each sequence, its new tokens' among them */
+    const int32_t *cu_seqlens;  /* in  [S+1] tokens as in ssd_gated_delta_step, or NULL: one each (T == S) */
+    int32_t *part_start;        /* out [S+1] first part of each sequence; [S] = number of parts */
+    int32_t *part_seq;          /* out [max_parts] sequence of each part; -1 past the last */
+    int32_t *part_keys;         /* out [1] keys of a part */
+    int32_t *error_flag;        /* in/out [1] sticky SSD_DATA_* bits */
+} ssd_attention_plan;
+
+/*
+ * Builds the plan. A sequence whose tokens are outside [0, total_tokens] or
+ * more than max_new_tokens sets SSD_DATA_BAD_CU_SEQLENS and is left out: the
+ * attention writes nothing for it. Negative seq_lens count as 0.
+ * Errors: SSD_ERR_NULL_ARG, SSD_ERR_SHAPE (sizes), SSD_ERR_CAPACITY
+ * (max_parts <= nseqs), SSD_ERR_HIP.
+ */
+ssd_status ssd_attention_plan_build(const ssd_attention_plan *plan, void *stream);
+
+/*
+ * Attention of each sequence's new tokens over its keys and values in a paged
+ * cache (their own were written before, by ssd_kv_cache_write): the attention
+ * layers of the hybrid models of the prefix-caching page, which share their
+ * step with the delta rule's. New token j of the n of sequence s has position
+ * p = seq_lens[s] - n + j. For query head h (kv head h / (nheads/nkvheads)):
+ *     o[t,h] = sum_i e_i v_i / sum_i e_i,   e_i = exp(scale q[t,h] . k_i),
+ * over the keys i <= p (and i > p - window, window > 0), and
+ *     lse[t,h] = log sum_i e_i.
+ * Tokens that see no key (an empty sequence, or p < 0), or only such whose
+ * products are all -infinity, get 0 and lse -infinity. What the cache holds
+ * where a token does not see it has no effect, whatever it is.
+ *  q, out          element type `dtype`, (total_tokens, nheads, head_dim), rows
+ *                  *_stride elements apart (at least the row, at most 2^26)
+ *  k_cache, v_cache  as in ssd_kv_cache_write, 16-byte aligned
+ *  block_table     int32 (table_rows, max_blocks), the blocks of row rows[s]
+ *                  (s when rows is NULL) in order
+ *  lse             float32 (total_tokens, nheads) or NULL
+ *  workspace       device memory, 16-byte aligned, of at least
+ *                  ssd_paged_attention_workspace_size bytes, owned by the
+ *                  caller: what the parts hand to the join. Calls that overlap
+ *                  in time need separate workspaces; nothing in it needs
+ *                  clearing.
+ *  error_flag      int32 [1] or NULL: a row outside the table sets
+ *                  SSD_DATA_BAD_SLOT (the sequence has no keys then); keys past
+ *                  the table's last column and blocks outside [0, num_blocks)
+ *                  set SSD_DATA_BAD_BLOCK and are left out.
+ * Supported: head_dim in {64, 128, 256}, block_size a multiple of 16 up to
+ * 2^20, num_blocks * block_size up to 2^31 - 1, nheads % nkvheads == 0.
+ * Precision: products' sums and the softmax's maxima and sums in float32. For bf16 the
+ * probabilities are rounded to bf16 before their product with the values. One
+ * rounding of the result. How a sequence is split, and with it its float32
+ * roundings, depends on the lengths of the whole batch, not on timing.
+ * Errors: SSD_ERR_NULL_ARG, SSD_ERR_DTYPE, SSD_ERR_SHAPE (sizes, strides,
+ * alignment, a scale that is not a number), SSD_ERR_BLOCK_SIZE,
+ * SSD_ERR_UNSUPPORTED (head_dim), SSD_ERR_CAPACITY (workspace, max_parts),
+ * SSD_ERR_HIP.
+ */
+ssd_status ssd_paged_attention_step(
+    const void *q, int64_t q_stride, const void *k_cache, const void *v_cache, ssd_dtype dtype, float scale,
+    const ssd_attention_plan *plan, int32_t nheads, int32_t nkvheads, int32_t head_dim, const int32_t *block_table,
+    int32_t table_rows, int32_t max_blocks, const int32_t *rows, int32_t num_blocks, int32_t block_size, void *out,
+    int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes, int32_t *error_flag, void *stream);
+
+/* Parts to aim at (max_parts - nseqs of a plan) so that a call with these heads fills the GPU. */
+int32_t ssd_paged_attention_parts(int32_t max_new_tokens, int32_t nheads, int32_t nkvheads);
+
+/* Workspace bytes that ssd_paged_attention_step needs for a plan of max_parts and max_new_tokens. */
+size_t ssd_paged_attention_workspace_size(int32_t max_parts, int32_t max_new_tokens, int32_t nheads, int32_t head_dim);
+
+/*
+ * RMS norm of rows with the residual's addition before it, as it stands
+ * between the layers of a stack, with an output in the inputs' type or in 8
+ * bits with scales. Per row:
+ *     r   = x + residual                          (x when residual is NULL)
+ *     n   = r / sqrt(mean(r^2) + eps) * weight
+ *     residual_out = r                            (not written when NULL)
+ *     out = n
+ *  x, residual, residual_out, out  element type `in_dtype`, (rows, channels),
+ *                  rows *_stride elements apart (at least channels, at most
+ *                  2^26). residual_out may be residual or x itself, out x itself.
+ *  weight          float32 (channels) or NULL (= 1)
+ * ssd_add_rms_norm_e4m3 gives n in 8 bits (e4m3: largest 448, with NaN, without
+ * infinities):
+ *     out = e4m3(n / scale), to nearest even, clamped to +-448
+ *  out             1 byte each, (rows, channels), rows out_stride bytes apart
+ *  scale           float32 [1] on the device: one given scale; or NULL:
+ *  scales          float32 (rows, channels/group), written: max |n| / 448 over
+ *                  each `group` consecutive channels, 1 where all are zero. A
+ *                  NaN among them makes the scale NaN. group == channels: one a row.
+ * Supported: channels 1 .. 16384; group == channels, or 32, 64, 128, 256 or 512
+ * where channels is a multiple of it; eps >= 0.
+ * Precision: float32; the norm takes r as it is before its rounding to
+ * residual_out; one rounding of each output.
+ * Errors: SSD_ERR_DTYPE, SSD_ERR_SHAPE (sizes, strides, alignment to the
+ * element, eps), SSD_ERR_UNSUPPORTED (channels, group), SSD_ERR_NULL_ARG,
+ * SSD_ERR_HIP.
+ */
+ssd_status ssd_add_rms_norm(
+    const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, const float *weight,
+    ssd_dtype in_dtype, int32_t rows, int32_t channels, float eps, void *residual_out, int64_t residual_out_stride,
+    void *out, int64_t out_stride, void *stream);
+
+ssd_status ssd_add_rms_norm_e4m3(
+    const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, const float *weight,
+    ssd_dtype in_dtype, int32_t rows, int32_t channels, int32_t group, float eps, const float *scale, float *scales,
+    void *residual_out, int64_t residual_out_stride, void *out, int64_t out_stride, void *stream);
 
 #ifdef __cplusplus
 }

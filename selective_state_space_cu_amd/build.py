@@ -13,7 +13,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libssd.so")
 SOURCES = ["ssd_api.hip", "ssd_meta.hip", "ssd_scan_bf16.hip", "ssd_scan_f32.hip",
            "ssd_scan_split_bf16.hip", "ssd_scan_ws_bf16.hip", "ssd_decode.hip", "ssd_conv1d.hip", "ssd_gdn.hip",
-           "ssd_selective.hip", "ssd_norm.hip"]
+           "ssd_selective.hip", "ssd_norm.hip", "ssd_gdn_step.hip", "ssd_attention.hip", "ssd_tables.hip",
+           "ssd_addnorm.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
          # no packed-fp32 instructions anywhere in the device code

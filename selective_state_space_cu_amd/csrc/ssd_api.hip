@@ -59,6 +59,52 @@ ssd_status check_selective(const ssd::SelectiveArgs &a, ssd_dtype in_dtype, ssd_
     return SSD_OK;
 }
 
+// What the calls on a paged cache ask of its sizes (`heads`: of q, or of the cache).
+ssd_status check_paged(int32_t heads, int32_t head_dim, int32_t num_blocks, int32_t block_size) {
+    if (heads <= 0 || head_dim <= 0 || num_blocks < 0) return SSD_ERR_SHAPE;
+    if (block_size < 16 || block_size % 16 != 0) return SSD_ERR_BLOCK_SIZE;
+    if (!(head_dim == 64 || head_dim == 128 || head_dim == 256)) return SSD_ERR_UNSUPPORTED;
+    if ((int64_t)num_blocks * block_size > INT32_MAX) return SSD_ERR_SHAPE;
+    return SSD_OK;
+}
+
+ssd_status check_plan(const ssd_attention_plan *p) {
+    if (p == nullptr || p->part_start == nullptr || p->part_seq == nullptr || p->part_keys == nullptr ||
+        p->error_flag == nullptr)
+        return SSD_ERR_NULL_ARG;
+    if (p->nseqs < 0 || p->total_tokens < 0 || p->max_new_tokens < 1 || p->max_new_tokens > 64 || p->window < 0 ||
+        p->max_parts > (1 << 26))
+        return SSD_ERR_SHAPE;
+    if (p->max_parts <= p->nseqs) return SSD_ERR_CAPACITY;
+    if (p->nseqs > 0 && p->seq_lens == nullptr) return SSD_ERR_NULL_ARG;
+    if (p->cu_seqlens == nullptr && p->total_tokens != p->nseqs) return SSD_ERR_SHAPE;
+    for (const void *q : {(const void *)p->seq_lens, (const void *)p->cu_seqlens, (const void *)p->part_start,
+                          (const void *)p->part_seq, (const void *)p->part_keys, (const void *)p->error_flag})
+        if (!aligned_to(q, 4)) return SSD_ERR_SHAPE;
+    return SSD_OK;
+}
+
+// Tiles of 16 rows (tokens x query heads of a kv head).
+int32_t attention_tiles(int32_t max_new_tokens, int32_t group) {
+    return (int32_t)(((int64_t)max_new_tokens * group + 15) / 16);
+}
+
+// What the two norms with a residual ask of their shared arguments.
+ssd_status check_add_norm(const ssd::AddNormArgs &a, ssd_dtype in_dtype) {
+    if (!known_dtype(in_dtype)) return SSD_ERR_DTYPE;
+    if (a.rows < 0 || a.channels <= 0 || !(a.eps >= 0.0f)) return SSD_ERR_SHAPE;
+    if (a.channels > ssd::kNormMaxGroup) return SSD_ERR_UNSUPPORTED;
+    if (a.rows == 0) return SSD_OK;
+    if (a.x == nullptr || a.out == nullptr) return SSD_ERR_NULL_ARG;
+    if (!row_stride(a.x_stride, a.channels) || !row_stride(a.out_stride, a.channels) ||
+        (a.residual != nullptr && !row_stride(a.residual_stride, a.channels)) ||
+        (a.residual_out != nullptr && !row_stride(a.residual_out_stride, a.channels)))
+        return SSD_ERR_SHAPE;
+    for (const void *p : {a.x, a.residual, (const void *)a.residual_out})
+        if (!aligned_to(p, elem_bytes(in_dtype))) return SSD_ERR_SHAPE;
+    return aligned_to(a.weight, 4) ? SSD_OK : SSD_ERR_SHAPE;
+}
+
 }  // namespace
 
 extern "C" {
@@ -69,11 +115,11 @@ const char *ssd_status_string(ssd_status status) {
     case SSD_ERR_NULL_ARG: return "a required pointer is NULL";
     case SSD_ERR_CHUNK_SIZE: return "chunk_size must be a power of two in [16, 256]";
     case SSD_ERR_SHAPE: return "invalid sizes, nheads % ngroups != 0, or a pointer not 16-byte aligned";
-    case SSD_ERR_BLOCK_SIZE: return "block_size must be a positive multiple of chunk_size";
-    case SSD_ERR_CAPACITY: return "capacity below the required bound (max_chunks or chunk_states)";
+    case SSD_ERR_BLOCK_SIZE: return "block_size must be a positive multiple of chunk_size (of 16 in a cache of keys and values)";
+    case SSD_ERR_CAPACITY: return "capacity below the required bound (max_chunks, chunk_states, max_parts or workspace)";
     case SSD_ERR_DTYPE: return "unknown dtype";
     case SSD_ERR_HIP: return "a HIP call failed";
-    case SSD_ERR_UNSUPPORTED: return "unsupported dtype/shape combination (headdim, dstate, dk, dv or chunk size)";
+    case SSD_ERR_UNSUPPORTED: return "unsupported dtype/shape combination (headdim, dstate, dk, dv, chunk size, channels or group)";
     }
     return "unknown status";
 }
@@ -436,6 +482,215 @@ ssd_status ssd_group_norm(const void *x, int64_t x_stride, const void *z, int64_
     a.rows = rows; a.groups = ngroups; a.size = channels / ngroups;
     a.eps = eps; a.center = center != 0; a.act = act;
     return ssd::launch_group_norm(a, in_dtype == SSD_BF16, static_cast<hipStream_t>(stream)) == hipSuccess
+               ? SSD_OK : SSD_ERR_HIP;
+}
+
+ssd_status ssd_gated_delta_step(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                int64_t v_stride, const void *gate, int64_t gate_stride, const void *beta,
+                                int64_t beta_stride, const float *A, const float *dt_bias, float qk_eps, float scale,
+                                ssd_dtype in_dtype, ssd_dtype gate_dtype, int32_t nseqs, int32_t total_tokens,
+                                const int32_t *cu_seqlens, int32_t nheads, int32_t nkheads, int32_t dk, int32_t dv,
+                                float *state_cache, int32_t num_slots, const int32_t *read_slot,
+                                const int32_t *write_slot, void *o, int64_t o_stride, int32_t *error_flag,
+                                void *stream) {
+    if (!known_dtype(in_dtype) || !known_dtype(gate_dtype)) return SSD_ERR_DTYPE;
+    if (nseqs < 0 || total_tokens < 0 || num_slots < 0 || nheads <= 0 || nkheads <= 0 || dk <= 0 || dv <= 0 ||
+        nheads % nkheads != 0 || qk_eps != qk_eps || scale != scale)
+        return SSD_ERR_SHAPE;
+    if (cu_seqlens == nullptr && total_tokens != nseqs) return SSD_ERR_SHAPE;
+    if (!(dk == 64 || dk == 128 || dk == 256)) return SSD_ERR_UNSUPPORTED;
+    if (nseqs == 0 || total_tokens == 0) return SSD_OK;
+    if (q == nullptr || k == nullptr || v == nullptr || gate == nullptr || beta == nullptr || o == nullptr ||
+        state_cache == nullptr || read_slot == nullptr || write_slot == nullptr)
+        return SSD_ERR_NULL_ARG;
+    const int64_t keys = (int64_t)nkheads * dk, values = (int64_t)nheads * dv;
+    if (!row_stride(q_stride, keys) || !row_stride(k_stride, keys) || !row_stride(v_stride, values) ||
+        !row_stride(o_stride, values) || !row_stride(gate_stride, nheads) || !row_stride(beta_stride, nheads))
+        return SSD_ERR_SHAPE;
+    for (const void *p : {q, k, v, (const void *)o})
+        if (!aligned_to(p, elem_bytes(in_dtype))) return SSD_ERR_SHAPE;
+    for (const void *p : {gate, beta})
+        if (!aligned_to(p, elem_bytes(gate_dtype))) return SSD_ERR_SHAPE;
+    for (const void *p : {(const void *)A, (const void *)dt_bias})
+        if (!aligned_to(p, 4)) return SSD_ERR_SHAPE;
+    if (!aligned16(state_cache)) return SSD_ERR_SHAPE;
+    ssd::GdnStepArgs a{};
+    a.q = q; a.k = k; a.v = v; a.gate = gate; a.beta = beta; a.A = A; a.dt_bias = dt_bias;
+    a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride; a.gate_stride = gate_stride;
+    a.beta_stride = beta_stride; a.o_stride = o_stride;
+    a.qk_eps = qk_eps; a.scale = scale; a.cu_seqlens = cu_seqlens; a.cache = state_cache;
+    a.read_slot = read_slot; a.write_slot = write_slot; a.o = o; a.error_flag = error_flag;
+    a.S = nseqs; a.T = total_tokens; a.H = nheads; a.G = nkheads; a.dv = dv; a.num_slots = num_slots;
+    return ssd::launch_gdn_step(a, in_dtype == SSD_BF16, gate_dtype == SSD_BF16, dk,
+                                static_cast<hipStream_t>(stream)) == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+
+ssd_status ssd_step_tables(int32_t nseqs, int32_t total_tokens, const int32_t *num_computed, const int32_t *num_new,
+                           const int32_t *rows, int32_t *block_table, int32_t table_rows, int32_t max_blocks,
+                           int32_t block_size, int32_t num_blocks, const int32_t *free_blocks, int32_t num_free,
+                           const int32_t *free_count, int32_t *free_count_out, int32_t *cu_seqlens,
+                           int32_t *seq_lens, int32_t *positions, int32_t *token_seq, int32_t *slots,
+                           int32_t *read_slot, int32_t *state_slot, int32_t *error_flag, void *stream) {
+    constexpr int32_t most = 1 << 20;
+    if (nseqs < 0 || nseqs > most || total_tokens < 0 || total_tokens > most || table_rows < 0 || max_blocks < 0 ||
+        max_blocks > most || num_blocks < 0 || num_free < 0 || num_free > (1 << 29))
+        return SSD_ERR_SHAPE;
+    if (block_size < 1) return SSD_ERR_BLOCK_SIZE;
+    if ((int64_t)num_blocks * block_size > INT32_MAX) return SSD_ERR_SHAPE;
+    if (cu_seqlens == nullptr || (free_blocks != nullptr && (free_count == nullptr || free_count_out == nullptr)))
+        return SSD_ERR_NULL_ARG;
+    if (nseqs > 0 && (num_computed == nullptr || num_new == nullptr || seq_lens == nullptr || read_slot == nullptr ||
+                      (block_table == nullptr && table_rows > 0 && max_blocks > 0)))
+        return SSD_ERR_NULL_ARG;
+    if (total_tokens > 0 && (positions == nullptr || token_seq == nullptr || slots == nullptr || state_slot == nullptr))
+        return SSD_ERR_NULL_ARG;
+    for (const void *p : {(const void *)num_computed, (const void *)num_new, (const void *)rows,
+                          (const void *)block_table, (const void *)free_blocks, (const void *)free_count,
+                          (const void *)free_count_out, (const void *)cu_seqlens, (const void *)seq_lens,
+                          (const void *)positions, (const void *)token_seq, (const void *)slots,
+                          (const void *)read_slot, (const void *)state_slot, (const void *)error_flag})
+        if (!aligned_to(p, 4)) return SSD_ERR_SHAPE;
+    ssd::TablesArgs a{};
+    a.num_computed = num_computed; a.num_new = num_new; a.rows = rows; a.block_table = block_table;
+    a.free_blocks = free_blocks; a.free_count = free_count; a.free_count_out = free_blocks ? free_count_out : nullptr;
+    a.cu_seqlens = cu_seqlens; a.seq_lens = seq_lens; a.positions = positions; a.token_seq = token_seq;
+    a.slots = slots; a.read_slot = read_slot; a.state_slot = state_slot; a.error_flag = error_flag;
+    a.S = nseqs; a.T = total_tokens; a.table_rows = table_rows; a.max_blocks = max_blocks; a.block = block_size;
+    a.num_blocks = num_blocks; a.num_free = num_free;
+    return ssd::launch_step_tables(a, static_cast<hipStream_t>(stream)) == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+
+ssd_status ssd_kv_cache_write(const void *k, int64_t k_stride, const void *v, int64_t v_stride, ssd_dtype dtype,
+                              int32_t total_tokens, int32_t nkvheads, int32_t head_dim, void *k_cache, void *v_cache,
+                              int32_t num_blocks, int32_t block_size, const int32_t *slots, int32_t *error_flag,
+                              void *stream) {
+    if (!known_dtype(dtype)) return SSD_ERR_DTYPE;
+    if (total_tokens < 0) return SSD_ERR_SHAPE;
+    const ssd_status st = check_paged(nkvheads, head_dim, num_blocks, block_size);
+    if (st != SSD_OK) return st;
+    if (total_tokens == 0) return SSD_OK;
+    if (k == nullptr || v == nullptr || slots == nullptr || (num_blocks > 0 && (k_cache == nullptr || v_cache == nullptr)))
+        return SSD_ERR_NULL_ARG;
+    const int64_t row = (int64_t)nkvheads * head_dim;
+    if (!row_stride(k_stride, row) || !row_stride(v_stride, row)) return SSD_ERR_SHAPE;
+    for (const void *p : {k, v})
+        if (!aligned_to(p, elem_bytes(dtype))) return SSD_ERR_SHAPE;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned_to(slots, 4)) return SSD_ERR_SHAPE;
+    ssd::KvWriteArgs a{};
+    a.k = k; a.v = v; a.k_stride = k_stride; a.v_stride = v_stride; a.k_cache = k_cache; a.v_cache = v_cache;
+    a.slots = slots; a.error_flag = error_flag;
+    a.T = total_tokens; a.Hkv = nkvheads; a.D = head_dim; a.block = block_size; a.num_slots = num_blocks * block_size;
+    return ssd::launch_kv_write(a, dtype == SSD_BF16, static_cast<hipStream_t>(stream)) == hipSuccess ? SSD_OK
+                                                                                                     : SSD_ERR_HIP;
+}
+
+ssd_status ssd_attention_plan_build(const ssd_attention_plan *plan, void *stream) {
+    const ssd_status st = check_plan(plan);
+    if (st != SSD_OK) return st;
+    ssd::AttnPlanArgs a{};
+    a.seq_lens = plan->seq_lens; a.cu_seqlens = plan->cu_seqlens; a.part_start = plan->part_start;
+    a.part_seq = plan->part_seq; a.part_keys = plan->part_keys; a.error_flag = plan->error_flag;
+    a.S = plan->nseqs; a.T = plan->total_tokens; a.max_new = plan->max_new_tokens; a.window = plan->window;
+    a.max_parts = plan->max_parts;
+    return ssd::launch_attention_plan(a, static_cast<hipStream_t>(stream)) == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+
+int32_t ssd_paged_attention_parts(int32_t max_new_tokens, int32_t nheads, int32_t nkvheads) {
+    if (max_new_tokens <= 0 || nheads <= 0 || nkvheads <= 0 || nheads % nkvheads != 0) return 0;
+    const int64_t per_part = (int64_t)nkvheads * attention_tiles(max_new_tokens, nheads / nkvheads);
+    return (int32_t)((ssd::kAttnWorkgroups + per_part - 1) / per_part);
+}
+
+size_t ssd_paged_attention_workspace_size(int32_t max_parts, int32_t max_new_tokens, int32_t nheads, int32_t head_dim) {
+    if (max_parts <= 0 || max_new_tokens <= 0 || nheads <= 0 || head_dim <= 0) return 0;
+    return (size_t)max_parts * (size_t)max_new_tokens * (size_t)nheads * ((size_t)head_dim + 2) * sizeof(float);
+}
+
+ssd_status ssd_paged_attention_step(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                                    ssd_dtype dtype, float scale, const ssd_attention_plan *plan, int32_t nheads,
+                                    int32_t nkvheads, int32_t head_dim, const int32_t *block_table,
+                                    int32_t table_rows, int32_t max_blocks, const int32_t *rows, int32_t num_blocks,
+                                    int32_t block_size, void *out, int64_t out_stride, float *lse, void *workspace,
+                                    size_t workspace_bytes, int32_t *error_flag, void *stream) {
+    ssd_status st = check_plan(plan);
+    if (st != SSD_OK) return st;
+    if (!known_dtype(dtype)) return SSD_ERR_DTYPE;
+    if (nheads <= 0 || nkvheads <= 0 || nheads % nkvheads != 0 || table_rows < 0 || max_blocks < 0 || scale != scale)
+        return SSD_ERR_SHAPE;
+    st = check_paged(nheads, head_dim, num_blocks, block_size);
+    if (st != SSD_OK) return st;
+    if (block_size > (1 << 20)) return SSD_ERR_BLOCK_SIZE;
+    if (plan->nseqs == 0 || plan->total_tokens == 0) return SSD_OK;
+    if (q == nullptr || out == nullptr || (num_blocks > 0 && (k_cache == nullptr || v_cache == nullptr)) ||
+        (table_rows > 0 && max_blocks > 0 && block_table == nullptr))
+        return SSD_ERR_NULL_ARG;
+    const int64_t row = (int64_t)nheads * head_dim;
+    if (!row_stride(q_stride, row) || !row_stride(out_stride, row)) return SSD_ERR_SHAPE;
+    for (const void *p : {q, (const void *)out})
+        if (!aligned_to(p, elem_bytes(dtype))) return SSD_ERR_SHAPE;
+    for (const void *p : {k_cache, v_cache, (const void *)workspace})
+        if (!aligned16(p)) return SSD_ERR_SHAPE;
+    for (const void *p : {(const void *)block_table, (const void *)rows, (const void *)lse})
+        if (!aligned_to(p, 4)) return SSD_ERR_SHAPE;
+    const size_t parts = (size_t)plan->max_parts * plan->max_new_tokens * nheads;
+    if (workspace == nullptr ||
+        workspace_bytes < ssd_paged_attention_workspace_size(plan->max_parts, plan->max_new_tokens, nheads, head_dim))
+        return SSD_ERR_CAPACITY;
+    ssd::AttnArgs a{};
+    a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.q_stride = q_stride; a.out_stride = out_stride;
+    a.seq_lens = plan->seq_lens; a.cu_seqlens = plan->cu_seqlens; a.part_start = plan->part_start;
+    a.part_seq = plan->part_seq; a.part_keys = plan->part_keys; a.block_table = block_table; a.rows = rows;
+    a.out = out; a.lse = lse;
+    a.part_o = static_cast<float *>(workspace); a.part_ml = a.part_o + parts * head_dim;
+    a.error_flag = error_flag; a.scale_log2 = scale * 1.4426950408889634f;
+    a.S = plan->nseqs; a.T = plan->total_tokens; a.max_new = plan->max_new_tokens; a.window = plan->window;
+    a.max_parts = plan->max_parts; a.Hq = nheads; a.Hkv = nkvheads; a.group = nheads / nkvheads;
+    a.tiles = attention_tiles(plan->max_new_tokens, a.group);
+    // no cache, no table: no keys
+    a.table_rows = num_blocks > 0 && max_blocks > 0 ? table_rows : 0;
+    a.max_blocks = max_blocks; a.num_blocks = num_blocks; a.block = block_size;
+    // exact division of 31-bit keys: 2^(31+L) / block rounded up has 32 bits, L = ceil(log2(block))
+    uint32_t L = 1;
+    while ((INT64_C(1) << L) < block_size) ++L;
+    a.block_magic = (uint32_t)(((UINT64_C(1) << (31 + L)) + block_size - 1) / block_size);
+    a.block_shift = L - 1;
+    return ssd::launch_attention(a, dtype == SSD_BF16, head_dim, static_cast<hipStream_t>(stream)) == hipSuccess
+               ? SSD_OK : SSD_ERR_HIP;
+}
+
+ssd_status ssd_add_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                            const float *weight, ssd_dtype in_dtype, int32_t rows, int32_t channels, float eps,
+                            void *residual_out, int64_t residual_out_stride, void *out, int64_t out_stride,
+                            void *stream) {
+    ssd::AddNormArgs a{};
+    a.x = x; a.residual = residual; a.weight = weight; a.residual_out = residual_out; a.out = out;
+    a.x_stride = x_stride; a.residual_stride = residual_stride; a.residual_out_stride = residual_out_stride;
+    a.out_stride = out_stride; a.rows = rows; a.channels = channels; a.group = channels; a.eps = eps;
+    const ssd_status st = check_add_norm(a, in_dtype);
+    if (st != SSD_OK || rows == 0) return st;
+    if (!aligned_to(out, elem_bytes(in_dtype))) return SSD_ERR_SHAPE;
+    return ssd::launch_add_rms_norm(a, in_dtype == SSD_BF16, false, static_cast<hipStream_t>(stream)) == hipSuccess
+               ? SSD_OK : SSD_ERR_HIP;
+}
+
+ssd_status ssd_add_rms_norm_e4m3(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                                 const float *weight, ssd_dtype in_dtype, int32_t rows, int32_t channels,
+                                 int32_t group, float eps, const float *scale, float *scales, void *residual_out,
+                                 int64_t residual_out_stride, void *out, int64_t out_stride, void *stream) {
+    ssd::AddNormArgs a{};
+    a.x = x; a.residual = residual; a.weight = weight; a.residual_out = residual_out; a.out = out;
+    a.scale = scale; a.scales = scales;
+    a.x_stride = x_stride; a.residual_stride = residual_stride; a.residual_out_stride = residual_out_stride;
+    a.out_stride = out_stride; a.rows = rows; a.channels = channels; a.group = group; a.eps = eps;
+    const ssd_status st = check_add_norm(a, in_dtype);
+    if (st != SSD_OK) return st;
+    if (group != channels && !((group == 32 || group == 64 || group == 128 || group == 256 || group == 512) &&
+                               channels % group == 0))
+        return SSD_ERR_UNSUPPORTED;
+    if (rows == 0) return SSD_OK;
+    if (scale == nullptr && scales == nullptr) return SSD_ERR_NULL_ARG;
+    if (!aligned_to(scale, 4) || !aligned_to(scales, 4)) return SSD_ERR_SHAPE;
+    return ssd::launch_add_rms_norm(a, in_dtype == SSD_BF16, true, static_cast<hipStream_t>(stream)) == hipSuccess
                ? SSD_OK : SSD_ERR_HIP;
 }
 

@@ -1,0 +1,449 @@
+// Attention of new tokens over a paged cache of keys and values, its split plan,
+// and the write of new keys and values to the cache.
+//   o_r = sum_j p_rj v_j / sum_j p_rj,  p_rj = exp(scale q_r . k_j),
+// over the keys j <= position of r's token (and > position - window).
+//
+// One pass with a running maximum and sum. A workgroup takes a part of one
+// sequence's keys for one kv head and 16 of its rows (tokens x query heads of the
+// kv head), its waves take steps of 32 keys (16 in float32) in turn, and the
+// parts of a sequence are joined by a second kernel. The split is planned on the
+// device from the lengths: parts of equal length over the whole batch, so that
+// there are enough of them whatever the lengths are.
+//
+// On the matrix cores both products are transposed, S^T = K Q^T and
+// O^T = V^T P^T, so that a row of the softmax is a column of the accumulators (its
+// maximum takes two lane exchanges, its factor none) and S^T is already the second
+// product's right operand: lane (g, q) of S^T holds keys W g .. W g + W - 1 of row q
+// once the rows of K are taken in the order key = W (q / 4) + 4 u + q mod 4 for the
+// W / 4 tiles u of a step. The cache holds values as (head dim, keys) so that the
+// left operand V^T is contiguous in memory too: keys and values go from memory to
+// the matrix cores through registers alone.
+#include "ssd_elem.hpp"
+
+namespace ssd {
+
+namespace {
+
+constexpr int kAttnWaves = 4;
+constexpr int kAttnThreads = 64 * kAttnWaves;
+constexpr int kPartUnit = 128;   // parts are whole multiples of this many keys
+
+template <typename T> struct Mma;
+template <> struct Mma<__bf16> {
+    __device__ static f32x4 mac(const u32x4 &a, const u32x4 &b, const f32x4 &c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+    // Probabilities are rounded to bf16 for the second product (2^-9 of each, the rounding of the output itself);
+    // their sum is taken before.
+    __device__ static u32x4 operand(const f32x4 (&p)[2]) {
+        return u32x4{pack_bf16(p[0][0], p[0][1]), pack_bf16(p[0][2], p[0][3]), pack_bf16(p[1][0], p[1][1]),
+                     pack_bf16(p[1][2], p[1][3])};
+    }
+};
+template <> struct Mma<float> {
+    __device__ static f32x4 mac(const u32x4 &a, const u32x4 &b, f32x4 c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0, 0, 0);
+        return c;
+    }
+    __device__ static u32x4 operand(const f32x4 (&p)[1]) { return __builtin_bit_cast(u32x4, p[0]); }
+};
+
+template <typename T> struct __attribute__((packed, aligned(sizeof(T)))) Raw16 { uint32_t w[4]; };
+
+// Tokens and keys of one sequence, as the plan and the kernels see them.
+struct Span {
+    int t0, n, len, lo;   // first token, tokens, keys, first key that any token sees (a multiple of 32)
+    bool bad;
+};
+
+__device__ __forceinline__ Span span_of(const int32_t *cu, const int32_t *lens, int s, int T, int max_new, int window) {
+    Span r;
+    r.t0 = cu != nullptr ? cu[s] : s;
+    const int t1 = cu != nullptr ? cu[s + 1] : s + 1;
+    r.bad = r.t0 < 0 || t1 < r.t0 || t1 > T || t1 - r.t0 > max_new;
+    r.n = r.bad ? 0 : t1 - r.t0;
+    r.len = max(lens[s], 0);
+    const int64_t lo = window > 0 ? (int64_t)r.len - r.n - window + 1 : 0;
+    r.lo = lo > 0 ? (int)lo & ~31 : 0;
+    return r;
+}
+
+__global__ __launch_bounds__(1024) void ssd_attention_plan_kernel(AttnPlanArgs a) {
+    __shared__ int64_t wave_sum[16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    auto scan = [&](int64_t v, int64_t &total) {   // inclusive
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int64_t o = __shfl_up(v, off, 64);
+            if (lane >= off) v += o;
+        }
+        __syncthreads();
+        if (lane == 63) wave_sum[wave] = v;
+        __syncthreads();
+        total = 0;
+        for (int w = 0; w < 16; ++w) {
+            if (w < wave) v += wave_sum[w];
+            total += wave_sum[w];
+        }
+        return v;
+    };
+    int64_t keys = 0;
+    for (int s = tid; s < a.S; s += 1024) {
+        const Span r = span_of(a.cu_seqlens, a.seq_lens, s, a.T, a.max_new, a.window);
+        if (r.bad) atomicOr(a.error_flag, SSD_DATA_BAD_CU_SEQLENS);
+        if (r.n > 0) keys += r.len - r.lo;
+    }
+    int64_t total;
+    scan(keys, total);
+    const int64_t target = a.max_parts - a.S;
+    const int64_t unit = ((total + target - 1) / target + kPartUnit - 1) / kPartUnit * kPartUnit;
+    const int part = (int)(unit < kPartUnit ? kPartUnit : unit);
+    int64_t carry = 0;
+    for (int base = 0; base < a.S; base += 1024) {
+        const int s = base + tid;
+        int64_t n = 0;
+        if (s < a.S) {
+            const Span r = span_of(a.cu_seqlens, a.seq_lens, s, a.T, a.max_new, a.window);
+            if (r.n > 0) n = max(((int64_t)r.len - r.lo + part - 1) / part, (int64_t)1);
+        }
+        const int64_t incl = scan(n, total);
+        if (s < a.S) a.part_start[s] = (int)(carry + incl - n);
+        carry += total;
+    }
+    if (tid == 0) {
+        a.part_start[a.S] = (int)carry;
+        *a.part_keys = part;
+    }
+    __syncthreads();
+    for (int p = tid; p < a.max_parts; p += 1024) {
+        int seq = -1;
+        if (p < carry) {
+            int lo = 0, hi = a.S;   // part_start[lo] <= p < part_start[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (a.part_start[mid] <= p) lo = mid; else hi = mid;
+            }
+            seq = lo;
+        }
+        a.part_seq[p] = seq;
+    }
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(kAttnThreads) void ssd_attention_kernel(AttnArgs a) {
+    constexpr int W = 16 / sizeof(T), U = W / 4, KEYS = 16 * U;   // elements of 16 bytes, 16-key tiles of a step, its keys
+    constexpr int CH = D / (4 * W), DB = D / 16;                  // 16-byte chunks of a key row and lane, blocks of 16 of D
+    constexpr int PAD = D + 4;
+    using M = Mma<T>;
+    __shared__ float red[kAttnWaves][16][PAD];
+    __shared__ float wave_m[kAttnWaves][16], wave_l[kAttnWaves][16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, q = lane & 15;
+    int b = blockIdx.x;
+    const int tile = b % a.tiles;
+    b /= a.tiles;
+    const int h = b % a.Hkv, p = b / a.Hkv;
+    const int s = a.part_seq[p];
+    if (s < 0) return;
+    const Span sp = span_of(a.cu_seqlens, a.seq_lens, s, a.T, a.max_new, a.window);
+    const int rows = sp.n * a.group;
+    if (tile * 16 >= rows) return;
+    const int first_part = a.part_start[s], nparts = a.part_start[s + 1] - first_part, part = *a.part_keys;
+    // keys that the table holds
+    const int trow = a.rows != nullptr ? a.rows[s] : s;
+    const bool row_ok = trow >= 0 && trow < a.table_rows;
+    const int64_t cap = row_ok ? (int64_t)a.max_blocks * a.block : 0;
+    const int len = (int)min((int64_t)sp.len, cap);
+    if (len < sp.len && p == first_part && h == 0 && tile == 0 && threadIdx.x == 0 && a.error_flag != nullptr)
+        atomicOr(a.error_flag, row_ok ? SSD_DATA_BAD_BLOCK : SSD_DATA_BAD_SLOT);
+    const int32_t *table = a.block_table + (int64_t)(row_ok ? trow : 0) * a.max_blocks;
+    const int64_t begin64 = sp.lo + (int64_t)(p - first_part) * part;
+    const int begin = (int)min(begin64, (int64_t)len), end = (int)min(begin64 + part, (int64_t)len);
+
+    // this lane's row (a column of the accumulators)
+    const int r = tile * 16 + q, token = min(r, rows - 1) / a.group;
+    const int hi = sp.len - sp.n + token, low = a.window > 0 ? hi - a.window + 1 : 0;
+    const int token0 = tile * 16 / a.group, token1 = min(tile * 16 + 15, rows - 1) / a.group;
+    const int all_hi = sp.len - sp.n + token0, all_low = a.window > 0 ? sp.len - sp.n + token1 - a.window + 1 : 0;
+    u32x4 qf[CH];
+    {
+        const int head = h * a.group + min(r, rows - 1) % a.group;
+        const T *at = reinterpret_cast<const T *>(a.q) + (sp.t0 + token) * a.q_stride + (int64_t)head * D + W * g;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const Raw16<T> v = *reinterpret_cast<const Raw16<T> *>(at + 4 * W * c);
+            qf[c] = r < rows ? u32x4{v.w[0], v.w[1], v.w[2], v.w[3]} : u32x4{0, 0, 0, 0};
+        }
+    }
+
+    struct Step {
+        u32x4 k[U][CH], v[DB];
+        bool ok;   // the block of this lane's keys is in the cache
+    };
+    const int64_t head_elems = (int64_t)a.block * D;
+    auto block_of = [&](int key) { return (int)(__umulhi((uint32_t)key, a.block_magic) >> a.block_shift); };
+    auto load = [&](Step &st, int key0) {
+        // keys past the end read the last ones again
+        const int vk = min(key0 + W * g, (len - 1) & ~(W - 1)), vb = block_of(vk);
+        const int kk = min(key0 + W * (q >> 2), (len - 1) & ~(W - 1)), kb = block_of(kk);
+        const int vid = table[vb], kid = table[kb];
+        st.ok = (uint32_t)vid < (uint32_t)a.num_blocks;
+        const int64_t vbase = ((int64_t)(st.ok ? vid : 0) * a.Hkv + h) * head_elems;
+        const int64_t kbase = ((int64_t)((uint32_t)kid < (uint32_t)a.num_blocks ? kid : 0) * a.Hkv + h) * head_elems;
+        const T *kp = reinterpret_cast<const T *>(a.k_cache) + kbase + W * g;
+        const T *vp = reinterpret_cast<const T *>(a.v_cache) + vbase + (vk - vb * a.block) + (int64_t)q * a.block;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = (int64_t)(kk - kb * a.block + 4 * u + (q & 3)) * D;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) st.k[u][c] = *reinterpret_cast<const u32x4 *>(kp + row + 4 * W * c);
+        }
+#pragma unroll
+        for (int db = 0; db < DB; ++db) st.v[db] = *reinterpret_cast<const u32x4 *>(vp + (int64_t)16 * db * a.block);
+    };
+
+    f32x4 o[DB];
+#pragma unroll
+    for (int db = 0; db < DB; ++db) o[db] = f32x4{0, 0, 0, 0};
+    float m = -INFINITY, l = 0.0f;   // of this lane's row; l over this lane's keys only
+    auto compute = [&](Step &st, int key0) {
+        f32x4 sc[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            sc[u] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int c = 0; c < CH; ++c) sc[u] = M::mac(st.k[u][c], qf[c], sc[u]);
+            sc[u] *= a.scale_log2;
+        }
+        const bool masked = key0 + KEYS - 1 > all_hi || key0 + KEYS > len || key0 < all_low || __any(!st.ok);   // uniform
+        if (masked) {
+            if (!st.ok && a.error_flag != nullptr) atomicOr(a.error_flag, SSD_DATA_BAD_BLOCK);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = key0 + W * g + 4 * u + i;
+                    if (!(st.ok && key <= hi && key >= low && key < len)) sc[u][i] = -INFINITY;
+                }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[u][i]);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        if (__any(top > m)) {
+            const float now = fmaxf(m, top), f = now == -INFINITY ? 1.0f : fast_exp2(m - now);
+            m = now;
+            l *= f;
+#pragma unroll
+            for (int db = 0; db < DB; ++db) o[db] *= f;
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sc[u][i] = fast_exp2(sc[u][i] - base);
+                l += sc[u][i];
+            }
+        const u32x4 pf = M::operand(sc);
+        if (!masked) {
+#pragma unroll
+            for (int db = 0; db < DB; ++db) o[db] = M::mac(st.v[db], pf, o[db]);
+        } else {
+            // What a token does not see may hold anything, and 0 x infinity is no 0: its values are cleared, token by
+            // token, and only that token's rows take the sum.
+            for (int t = token0; t <= token1; ++t) {
+                const int t_hi = min(sp.len - sp.n + t, len - 1), t_low = a.window > 0 ? sp.len - sp.n + t - a.window + 1 : 0;
+                uint32_t seen[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = key0 + W * g + i * (W / 4);
+                    auto one = [&](int at) { return st.ok && at <= t_hi && at >= t_low; };
+                    seen[i] = W == 4 ? (one(key) ? 0xffffffffu : 0u)
+                                     : (one(key) ? 0x0000ffffu : 0u) | (one(key + 1) ? 0xffff0000u : 0u);
+                }
+#pragma unroll
+                for (int db = 0; db < DB; ++db) {
+                    const u32x4 v = st.v[db];
+                    const f32x4 with = M::mac(u32x4{v[0] & seen[0], v[1] & seen[1], v[2] & seen[2], v[3] & seen[3]}, pf, o[db]);
+                    if (token == t) o[db] = with;
+                }
+            }
+        }
+    };
+
+    constexpr int STRIDE = KEYS * kAttnWaves;
+    for (int key = begin + wave * KEYS; key < end; key += STRIDE) {
+        Step st;
+        load(st, key);
+        compute(st, key);
+    }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+
+    // join the waves
+    if (g == 0) {
+        wave_m[wave][q] = m;
+        wave_l[wave][q] = l;
+    }
+    __syncthreads();
+    float top = -INFINITY;
+    for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, wave_m[w][q]);
+    const float f = top == -INFINITY ? 0.0f : fast_exp2(m - top);
+#pragma unroll
+    for (int db = 0; db < DB; ++db) *reinterpret_cast<f32x4 *>(&red[wave][q][16 * db + 4 * g]) = o[db] * f;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * D / 4; i += kAttnThreads) {
+        const int row = i / (D / 4), d = i % (D / 4) * 4, rr = tile * 16 + row;
+        if (rr >= rows) break;
+        float best = -INFINITY, sum = 0.0f;
+        for (int w = 0; w < kAttnWaves; ++w) best = fmaxf(best, wave_m[w][row]);
+        f32x4 v{0, 0, 0, 0};
+        for (int w = 0; w < kAttnWaves; ++w) {
+            sum += best == -INFINITY ? 0.0f : wave_l[w][row] * fast_exp2(wave_m[w][row] - best);
+            v += *reinterpret_cast<const f32x4 *>(&red[w][row][d]);
+        }
+        if (nparts == 1) {
+            const int64_t t = sp.t0 + rr / a.group;
+            const int head = h * a.group + rr % a.group;
+            T *out = reinterpret_cast<T *>(a.out) + t * a.out_stride + (int64_t)head * D + d;
+            const float inv = best == -INFINITY ? 0.0f : 1.0f / sum;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) out[k] = (T)(v[k] * inv);
+            if (a.lse != nullptr && d == 0) a.lse[t * a.Hq + head] = (best + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+        } else {
+            const int64_t at = ((int64_t)p * a.Hkv + h) * a.max_new * a.group + rr;
+            *reinterpret_cast<f32x4 *>(a.part_o + at * D + d) = v;
+            if (d == 0) {
+                a.part_ml[2 * at] = best;
+                a.part_ml[2 * at + 1] = sum;
+            }
+        }
+    }
+}
+
+// Joins the parts of sequences that have several: one workgroup per token and head.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void ssd_attention_join_kernel(AttnArgs a) {
+    constexpr int LANES = D / 4, GROUPS = 256 / LANES;
+    __shared__ float red[GROUPS][D], red_m[GROUPS], red_l[GROUPS];
+    const int t = blockIdx.x / a.Hq, head = blockIdx.x % a.Hq;
+    int s = t;
+    if (a.cu_seqlens != nullptr) {
+        int lo = 0, hi = a.S;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.cu_seqlens[mid] <= t) lo = mid; else hi = mid;
+        }
+        s = lo;
+    }
+    const Span sp = span_of(a.cu_seqlens, a.seq_lens, s, a.T, a.max_new, a.window);
+    if (t < sp.t0 || t >= sp.t0 + sp.n) return;
+    const int first = a.part_start[s], nparts = a.part_start[s + 1] - first;
+    if (nparts <= 1) return;
+    const int rows = a.max_new * a.group, r = (t - sp.t0) * a.group + head % a.group, h = head / a.group;
+    const int grp = threadIdx.x / LANES, d = threadIdx.x % LANES * 4;
+    float m = -INFINITY, l = 0.0f;
+    f32x4 v{0, 0, 0, 0};
+    for (int k = grp; k < nparts; k += GROUPS) {
+        const int64_t at = ((int64_t)(first + k) * a.Hkv + h) * rows + r;
+        const float pm = a.part_ml[2 * at], pl = a.part_ml[2 * at + 1];
+        const f32x4 pv = *reinterpret_cast<const f32x4 *>(a.part_o + at * D + d);
+        const float now = fmaxf(m, pm);
+        if (now == -INFINITY) continue;
+        const float f = fast_exp2(m - now), e = fast_exp2(pm - now);
+        m = now;
+        l = l * f + pl * e;
+        v = v * f + pv * e;
+    }
+    *reinterpret_cast<f32x4 *>(&red[grp][d]) = v;
+    if (d == 0) {
+        red_m[grp] = m;
+        red_l[grp] = l;
+    }
+    __syncthreads();
+    if (grp != 0) return;
+    float best = -INFINITY, sum = 0.0f;
+    for (int k = 0; k < GROUPS; ++k) best = fmaxf(best, red_m[k]);
+    v = f32x4{0, 0, 0, 0};
+    for (int k = 0; k < GROUPS; ++k) {
+        const float e = best == -INFINITY ? 0.0f : fast_exp2(red_m[k] - best);
+        sum += red_l[k] * e;
+        v += *reinterpret_cast<const f32x4 *>(&red[k][d]) * e;
+    }
+    T *out = reinterpret_cast<T *>(a.out) + t * a.out_stride + (int64_t)head * D + d;
+    const float inv = best == -INFINITY ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) out[k] = (T)(v[k] * inv);
+    if (a.lse != nullptr && d == 0) a.lse[(int64_t)t * a.Hq + head] = (best + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+}
+
+// Copies the rows of new tokens to their slots: keys as they are, values turned.
+template <typename T>
+__global__ __launch_bounds__(256) void ssd_kv_write_kernel(KvWriteArgs a) {
+    constexpr int W = 16 / sizeof(T);
+    const int per = a.Hkv * a.D / W;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t t = i / per;
+    if (t >= a.T) return;
+    const int e = (int)(i - t * per) * W, h = e / a.D, d = e % a.D;
+    const int slot = a.slots[t];
+    if (slot < 0) return;
+    if (slot >= a.num_slots) {
+        if (e == 0 && a.error_flag != nullptr) atomicOr(a.error_flag, SSD_DATA_BAD_SLOT);
+        return;
+    }
+    const int block = slot / a.block, at = slot - block * a.block;
+    const Raw16<T> k = *reinterpret_cast<const Raw16<T> *>(reinterpret_cast<const T *>(a.k) + t * a.k_stride + e);
+    const T *v = reinterpret_cast<const T *>(a.v) + t * a.v_stride + e;
+    const int64_t head = ((int64_t)block * a.Hkv + h) * a.block * a.D;
+    *reinterpret_cast<Raw16<T> *>(reinterpret_cast<T *>(a.k_cache) + head + (int64_t)at * a.D + d) = k;
+    T *vc = reinterpret_cast<T *>(a.v_cache) + head + (int64_t)d * a.block + at;
+#pragma unroll
+    for (int j = 0; j < W; ++j) vc[(int64_t)j * a.block] = v[j];
+}
+
+template <typename T, int D> hipError_t launch_attention_d(const AttnArgs &a, hipStream_t stream) {
+    const int64_t blocks = (int64_t)a.max_parts * a.Hkv * a.tiles, joins = (int64_t)a.T * a.Hq;
+    if (!fits_grid(blocks, kAttnThreads) || !fits_grid(joins, 256)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((ssd_attention_kernel<T, D>), dim3((unsigned)blocks), dim3(kAttnThreads), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((ssd_attention_join_kernel<T, D>), dim3((unsigned)joins), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t launch_attention_t(const AttnArgs &a, int D, hipStream_t stream) {
+    switch (D) {
+        case 64: return launch_attention_d<T, 64>(a, stream);
+        case 128: return launch_attention_d<T, 128>(a, stream);
+        case 256: return launch_attention_d<T, 256>(a, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_attention_plan(const AttnPlanArgs &a, hipStream_t stream) {
+    hipLaunchKernelGGL(ssd_attention_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_attention(const AttnArgs &a, bool bf16, int D, hipStream_t stream) {
+    return bf16 ? launch_attention_t<__bf16>(a, D, stream) : launch_attention_t<float>(a, D, stream);
+}
+
+hipError_t launch_kv_write(const KvWriteArgs &a, bool bf16, hipStream_t stream) {
+    const int64_t lanes = (int64_t)a.T * a.Hkv * a.D / (bf16 ? 8 : 4);
+    const int64_t blocks = (lanes + 255) / 256;
+    if (!fits_grid(blocks, 256)) return hipErrorInvalidConfiguration;
+    if (bf16) hipLaunchKernelGGL((ssd_kv_write_kernel<__bf16>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((ssd_kv_write_kernel<float>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace ssd

@@ -1,0 +1,154 @@
+// Gated delta rule token by token, with dual state anchors: the new tokens of
+// every sequence (one, or a few speculated ones) advance the state read from one
+// cache slot, and the state after each token that has a write slot goes there.
+// Per value head h (key head g = h / (H/G)), with the state S (dv x dk):
+//   S'  = alpha S + beta (v - alpha S k) k^T,   o = scale S' q
+// Both products need only the entering state, so one pass over S gives them:
+//   r = S k, w = S q;  d = beta (v - alpha r);  S' = alpha S + d k^T;
+//   o = scale (alpha w + d (k . q))
+// q and k may still have to be normed: k = kn k_raw, kn = 1 / sqrt(|k_raw|^2 + eps).
+//
+// Memory-bound: the states are the traffic (4 dk dv bytes read and written per
+// (sequence, head)). Eight lanes own a state row, in float4 pieces 8 lanes apart,
+// so that eight rows of a wave's access are whole 128-byte lines, and the two
+// sums over a row take three lane exchanges each.
+#include "ssd_elem.hpp"
+
+namespace ssd {
+
+constexpr int kGdnStepThreads = 128;
+constexpr int kGdnStepRows = 2;     // state rows of a lane
+
+// Sum over the 8 lanes of a row; every lane gets it.
+__device__ __forceinline__ float sum8(float v) {
+    auto add = [&](auto ctrl) {
+        v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    add(std::integral_constant<int, 0xB1>{});    // lane ^ 1
+    add(std::integral_constant<int, 0x4E>{});    // lane ^ 2
+    add(std::integral_constant<int, 0x141>{});   // 7 - lane
+    return v;
+}
+
+template <typename T, typename GT, int DK, int R>
+__global__ __launch_bounds__(kGdnStepThreads) void ssd_gdn_step_kernel(GdnStepArgs a) {
+    constexpr int PIECES = DK / 32, GROUPS = kGdnStepThreads / 8;
+    using E = RawOf<T>;
+    const int lr = threadIdx.x % 8, rg = threadIdx.x / 8;
+    int64_t b = blockIdx.x;
+    const int rb = (int)(b % a.row_blocks);
+    b /= a.row_blocks;
+    const int h = (int)(b % a.H), s = (int)(b / a.H);
+    const bool first = rb == 0 && h == 0 && threadIdx.x == 0;   // speaks for the sequence
+    int t0 = s, t1 = s + 1;
+    if (a.cu_seqlens != nullptr) {
+        t0 = a.cu_seqlens[s];
+        t1 = a.cu_seqlens[s + 1];
+        if (t0 < 0 || t1 < t0 || t1 > a.T) {
+            if (first && a.error_flag != nullptr) atomicOr(a.error_flag, SSD_DATA_BAD_CU_SEQLENS);
+            return;
+        }
+    }
+    if (t0 == t1) return;
+    const int rs = a.read_slot[s];
+    bool bad = rs >= a.num_slots;
+    for (int t = t0 + (int)threadIdx.x; t < t1; t += kGdnStepThreads) bad |= a.write_slot[t] >= a.num_slots;
+    if (__syncthreads_or(bad)) {   // refused: nothing read or written
+        if (first && a.error_flag != nullptr) atomicOr(a.error_flag, SSD_DATA_BAD_SLOT);
+        return;
+    }
+    const int g = h / (a.H / a.G);
+    const int p0 = rb * GROUPS * R + rg;   // rows p0, p0 + GROUPS, ..
+    const int64_t slot = (int64_t)a.H * a.dv * DK, head = (int64_t)h * a.dv * DK + 4 * lr;
+    f32x4 st[R][PIECES];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int p = p0 + r * GROUPS;
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j)
+            st[r][j] = rs >= 0 && p < a.dv
+                           ? __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(a.cache + rs * slot + head + (int64_t)p * DK + 32 * j))
+                           : f32x4{0, 0, 0, 0};
+    }
+    for (int t = t0; t < t1; ++t) {
+        f32x4 k[PIECES], q[PIECES];
+        float kk = 0.0f, qq = 0.0f, kq = 0.0f;
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+            const int64_t n = (int64_t)g * DK + 32 * j + 4 * lr;
+            k[j] = E::f4(*reinterpret_cast<const typename E::Four *>(reinterpret_cast<const T *>(a.k) + t * a.k_stride + n));
+            q[j] = E::f4(*reinterpret_cast<const typename E::Four *>(reinterpret_cast<const T *>(a.q) + t * a.q_stride + n));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                kk = fmaf(k[j][i], k[j][i], kk);
+                qq = fmaf(q[j][i], q[j][i], qq);
+                kq = fmaf(k[j][i], q[j][i], kq);
+            }
+        }
+        float gate = load_f<GT>(a.gate, t * a.gate_stride + h), beta = load_f<GT>(a.beta, t * a.beta_stride + h);
+        if (a.A != nullptr) {
+            gate = a.A[h] * softplus_full(gate + (a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f));
+            beta = 1.0f / (1.0f + fast_exp2(-beta * kLog2e));
+        }
+        const float alpha = fast_exp2(gate * kLog2e);
+        kq = sum8(kq);
+        float kn = 1.0f, qn = a.scale;
+        if (a.qk_eps >= 0.0f) {
+            kn = 1.0f / sqrtf(sum8(kk) + a.qk_eps);
+            qn *= 1.0f / sqrtf(sum8(qq) + a.qk_eps);
+        }
+        const int ws = a.write_slot[t];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int p = p0 + r * GROUPS;
+            float sk = 0.0f, sq = 0.0f;
+#pragma unroll
+            for (int j = 0; j < PIECES; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sk = fmaf(st[r][j][i], k[j][i], sk);
+                    sq = fmaf(st[r][j][i], q[j][i], sq);
+                }
+            sk = sum8(sk);
+            sq = sum8(sq);
+            if (p >= a.dv) continue;
+            const float v = load_f<T>(a.v, t * a.v_stride + (int64_t)h * a.dv + p);
+            const float d = beta * (v - alpha * kn * sk) * kn;
+            if (lr == 0)
+                reinterpret_cast<T *>(a.o)[t * a.o_stride + (int64_t)h * a.dv + p] = (T)(qn * fmaf(alpha, sq, d * kq));
+#pragma unroll
+            for (int j = 0; j < PIECES; ++j) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) st[r][j][i] = fmaf(alpha, st[r][j][i], d * k[j][i]);
+                if (ws >= 0)
+                    __builtin_nontemporal_store(st[r][j], reinterpret_cast<f32x4 *>(a.cache + ws * slot + head + (int64_t)p * DK + 32 * j));
+            }
+        }
+    }
+}
+
+template <typename T, typename GT, int DK> static hipError_t launch_gdn_step_rows(GdnStepArgs a, hipStream_t stream) {
+    constexpr int ROWS = kGdnStepThreads / 8 * kGdnStepRows;
+    a.row_blocks = (a.dv + ROWS - 1) / ROWS;
+    const int64_t blocks = (int64_t)a.S * a.H * a.row_blocks;
+    if (!fits_grid(blocks, kGdnStepThreads)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((ssd_gdn_step_kernel<T, GT, DK, kGdnStepRows>), dim3((unsigned)blocks), dim3(kGdnStepThreads), 0,
+                       stream, a);
+    return hipGetLastError();
+}
+
+template <typename T, typename GT> static hipError_t launch_gdn_step_t(const GdnStepArgs &a, int dk, hipStream_t stream) {
+    switch (dk) {
+        case 64: return launch_gdn_step_rows<T, GT, 64>(a, stream);
+        case 128: return launch_gdn_step_rows<T, GT, 128>(a, stream);
+        case 256: return launch_gdn_step_rows<T, GT, 256>(a, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_gdn_step(const GdnStepArgs &a, bool bf16, bool gate_bf16, int dk, hipStream_t stream) {
+    if (bf16) return gate_bf16 ? launch_gdn_step_t<__bf16, __bf16>(a, dk, stream) : launch_gdn_step_t<__bf16, float>(a, dk, stream);
+    return gate_bf16 ? launch_gdn_step_t<float, __bf16>(a, dk, stream) : launch_gdn_step_t<float, float>(a, dk, stream);
+}
+
+}  // namespace ssd

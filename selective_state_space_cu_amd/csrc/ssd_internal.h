@@ -189,6 +189,82 @@ struct NormArgs {
 constexpr int32_t kNormMaxGroup = 16384;
 hipError_t launch_group_norm(const NormArgs &a, bool bf16, hipStream_t stream);
 
+// Gated delta rule token by token (see ssd_gdn_step.hip).
+struct GdnStepArgs {
+    const void *q, *k, *v, *gate, *beta;
+    const float *A, *dt_bias;           // A null: gate is the log-decay and beta the write strength
+    int64_t q_stride, k_stride, v_stride, gate_stride, beta_stride, o_stride;   // elements between rows
+    float qk_eps, scale;                // qk_eps < 0: q and k as they are
+    const int32_t *cu_seqlens;          // (S+1) or null: one token per sequence
+    float *cache;                       // (num_slots, H, dv, dk)
+    const int32_t *read_slot, *write_slot;   // (S), (T)
+    void *o;
+    int32_t *error_flag;                // nullable
+    int32_t S, T, H, G, dv, num_slots, row_blocks;   // row_blocks: workgroups per (sequence, head)
+};
+hipError_t launch_gdn_step(const GdnStepArgs &a, bool bf16, bool gate_bf16, int dk, hipStream_t stream);
+
+// Paged key-value cache and the attention over it (see ssd_attention.hip).
+struct KvWriteArgs {
+    const void *k, *v;
+    int64_t k_stride, v_stride;         // elements between tokens
+    void *k_cache, *v_cache;            // (num_blocks, Hkv, block, D), (num_blocks, Hkv, D, block)
+    const int32_t *slots;               // (T)
+    int32_t *error_flag;                // nullable
+    int32_t T, Hkv, D, block, num_slots;   // num_slots: num_blocks * block
+};
+hipError_t launch_kv_write(const KvWriteArgs &a, bool bf16, hipStream_t stream);
+
+struct AttnPlanArgs {
+    const int32_t *seq_lens, *cu_seqlens;   // cu_seqlens null: one token per sequence
+    int32_t *part_start, *part_seq, *part_keys, *error_flag;
+    int32_t S, T, max_new, window, max_parts;
+};
+hipError_t launch_attention_plan(const AttnPlanArgs &a, hipStream_t stream);
+
+struct AttnArgs {
+    const void *q, *k_cache, *v_cache;
+    int64_t q_stride, out_stride;       // elements between tokens
+    const int32_t *seq_lens, *cu_seqlens, *part_start, *part_seq, *part_keys;
+    const int32_t *block_table, *rows;  // rows null: sequence s has row s
+    void *out;
+    float *lse;                         // (T, Hq) or null
+    float *part_o, *part_ml;            // workspace: (parts, Hkv, rows, D) and (parts, Hkv, rows, 2)
+    int32_t *error_flag;
+    float scale_log2;                   // scale times log2 e
+    int32_t S, T, max_new, window, max_parts, Hq, Hkv, group, tiles;
+    int32_t table_rows, max_blocks, num_blocks, block;
+    uint32_t block_magic, block_shift;  // key / block = mulhi(key, block_magic) >> block_shift, for 31-bit keys
+};
+// Workgroups that an attention call aims at: 4 for each of the 256 CUs.
+constexpr int32_t kAttnWorkgroups = 1024;
+hipError_t launch_attention(const AttnArgs &a, bool bf16, int D, hipStream_t stream);
+
+// Block tables and slot maps of one step (see ssd_tables.hip).
+struct TablesArgs {
+    const int32_t *num_computed, *num_new, *rows;   // rows null: request s has row s
+    int32_t *block_table;
+    const int32_t *free_blocks, *free_count;        // free_blocks null: nothing is allocated
+    int32_t *free_count_out;
+    int32_t *cu_seqlens, *seq_lens, *positions, *token_seq, *slots, *read_slot, *state_slot;
+    int32_t *error_flag;
+    int32_t S, T, table_rows, max_blocks, block, num_blocks, num_free;
+};
+hipError_t launch_step_tables(const TablesArgs &a, hipStream_t stream);
+
+// RMS norm of rows with the residual's addition (see ssd_addnorm.hip).
+struct AddNormArgs {
+    const void *x, *residual;           // residual null: x alone
+    const float *weight;                // nullable
+    void *residual_out, *out;           // residual_out null: not written; out: type of x, or e4m3 with scales
+    const float *scale;                 // e4m3: given scale (1), or null: scales are computed
+    float *scales;                      // e4m3: (rows, channels / group)
+    int64_t x_stride, residual_stride, residual_out_stride, out_stride;
+    int32_t rows, channels, group;      // group: channels that share a scale
+    float eps;
+};
+hipError_t launch_add_rms_norm(const AddNormArgs &a, bool bf16, bool e4m3, hipStream_t stream);
+
 struct MetaArgs {
     const int32_t *cu_seqlens;
     int32_t *chunk_offsets, *chunk_seq_idx, *seq_chunk_start, *nchunks, *seq_order, *error_flag;

@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libssd.so")
 
 SSD_F32, SSD_BF16 = 0, 1
 NORM_ACTS = {"none": 0, "silu": 1, "gate_first": 2, "gate_last": 3}   # ssd_norm_act
-DATA_BAD_CU_SEQLENS, DATA_TOO_MANY_CHUNKS, DATA_BAD_SLOT, DATA_BAD_BLOCK = 1, 2, 4, 8
+DATA_BAD_CU_SEQLENS, DATA_TOO_MANY_CHUNKS, DATA_BAD_SLOT, DATA_BAD_BLOCK, DATA_NO_BLOCK = 1, 2, 4, 8, 16
 
 # names exported by libssd.so (checked by the CPU tests against include/ssd.h)
 EXPORTS = ("ssd_varlen_metadata", "ssd_chunk_scan_varlen", "ssd_export_chunk_states",
@@ -26,6 +26,9 @@ EXPORTS = ("ssd_varlen_metadata", "ssd_chunk_scan_varlen", "ssd_export_chunk_sta
            "ssd_gated_delta_chunk_varlen_noalloc",
            "ssd_prefill_bites",
            "ssd_selective_scan_varlen", "ssd_selective_step", "ssd_causal_conv1d_step", "ssd_group_norm",
+           "ssd_gated_delta_step", "ssd_step_tables", "ssd_kv_cache_write", "ssd_attention_plan_build",
+           "ssd_paged_attention_step", "ssd_paged_attention_parts", "ssd_paged_attention_workspace_size",
+           "ssd_add_rms_norm", "ssd_add_rms_norm_e4m3",
            "ssd_status_string")
 
 
@@ -44,6 +47,13 @@ class _Meta(ctypes.Structure):
                 ("chunk_seq_idx", ctypes.c_void_p), ("seq_chunk_start", ctypes.c_void_p),
                 ("nchunks", ctypes.c_void_p), ("seq_order", ctypes.c_void_p),
                 ("error_flag", ctypes.c_void_p)]
+
+
+class _Plan(ctypes.Structure):
+    _fields_ = [("nseqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32), ("max_new_tokens", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("max_parts", ctypes.c_int32), ("seq_lens", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("part_start", ctypes.c_void_p), ("part_seq", ctypes.c_void_p),
+                ("part_keys", ctypes.c_void_p), ("error_flag", ctypes.c_void_p)]
 
 
 _lib = None
@@ -97,6 +107,28 @@ def load_library(path: str = LIB_PATH):
     lib.ssd_causal_conv1d_step.argtypes = [vp, i64, vp, vp, st, i32, i32, i32, i32, vp, i32, vp, vp, vp, i64, vp, vp]
     lib.ssd_group_norm.restype = st
     lib.ssd_group_norm.argtypes = [vp, i64, vp, i64, vp, vp, st, i32, i32, i32, ctypes.c_float, i32, st, vp, i64, vp]
+    f32, size = ctypes.c_float, ctypes.c_size_t
+    lib.ssd_gated_delta_step.restype = st
+    lib.ssd_gated_delta_step.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, f32, f32, st, st, i32, i32,
+                                         vp, i32, i32, i32, i32, vp, i32, vp, vp, vp, i64, vp, vp]
+    lib.ssd_step_tables.restype = st
+    lib.ssd_step_tables.argtypes = [i32, i32, vp, vp, vp, vp, i32, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp,
+                                    vp, vp, vp]
+    lib.ssd_kv_cache_write.restype = st
+    lib.ssd_kv_cache_write.argtypes = [vp, i64, vp, i64, st, i32, i32, i32, vp, vp, i32, i32, vp, vp, vp]
+    lib.ssd_attention_plan_build.restype = st
+    lib.ssd_attention_plan_build.argtypes = [ctypes.POINTER(_Plan), vp]
+    lib.ssd_paged_attention_step.restype = st
+    lib.ssd_paged_attention_step.argtypes = [vp, i64, vp, vp, st, f32, ctypes.POINTER(_Plan), i32, i32, i32, vp, i32,
+                                             i32, vp, i32, i32, vp, i64, vp, vp, size, vp, vp]
+    lib.ssd_paged_attention_parts.restype = i32
+    lib.ssd_paged_attention_parts.argtypes = [i32, i32, i32]
+    lib.ssd_paged_attention_workspace_size.restype = size
+    lib.ssd_paged_attention_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.ssd_add_rms_norm.restype = st
+    lib.ssd_add_rms_norm.argtypes = [vp, i64, vp, i64, vp, st, i32, i32, f32, vp, i64, vp, i64, vp]
+    lib.ssd_add_rms_norm_e4m3.restype = st
+    lib.ssd_add_rms_norm_e4m3.argtypes = [vp, i64, vp, i64, vp, st, i32, i32, i32, f32, vp, vp, vp, i64, vp, i64, vp]
     lib.ssd_prefill_bites.restype = st
     lib.ssd_prefill_bites.argtypes = [i32, vp, vp, vp, i32, vp]
     _lib = lib
@@ -670,3 +702,294 @@ def group_norm(x: torch.Tensor, ngroups: int, weight: Optional[torch.Tensor] = N
              _dtype_code(x), shape[0], channels, int(ngroups), float(eps), 1 if center else 0, NORM_ACTS[act],
              out.data_ptr(), out_stride)
     return out
+
+
+def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gate: torch.Tensor, beta: torch.Tensor,
+                     state_cache: torch.Tensor, read_slot: torch.Tensor, write_slot: torch.Tensor,
+                     cu_seqlens: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                     A: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
+                     qk_eps: Optional[float] = None, o: Optional[torch.Tensor] = None,
+                     error_flag: Optional[torch.Tensor] = None):
+    """ssd_gated_delta_step: the gated delta rule for the new tokens of every sequence (one each, or cu_seqlens). The
+    state is read from state_cache[read_slot[s]] (zero if < 0); after token t it is written to
+    state_cache[write_slot[t]] (skipped if < 0). q, k (T, G, dk), v (T, H, dv), gate, beta (T, H) (float32 or bf16) may be
+    slices with rows further apart; state_cache float32 (slots, H, dv, dk), read_slot (S,), write_slot (T,). With A (H,),
+    gate and beta are raw: the log-decay is A softplus(gate + dt_bias) and the strength sigmoid(beta). With qk_eps, q and
+    k are divided by sqrt(|.|^2 + qk_eps). scale: dk ** -0.5 unless given. Returns o (T, H, dv)."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"q must be (tokens, key heads, dk) and v (tokens, heads, dv), got {tuple(q.shape)} and "
+                         f"{tuple(v.shape)}")
+    device, dtype, vshape, qshape = v.device, v.dtype, v.shape, q.shape
+    tokens, heads, dv = vshape
+    qtokens, kheads, dk = qshape
+    if qtokens != tokens:
+        raise ValueError(f"q must have {tokens} tokens, got {qtokens}")
+    code = _dtype_code(v)
+    if gate.dtype != dtype and gate.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"gate must be float32 or bfloat16, got {gate.dtype}")
+    if A is None and dt_bias is not None:
+        raise ValueError("dt_bias is given only with A")
+    if qk_eps is not None and not qk_eps >= 0:
+        raise ValueError(f"qk_eps must not be negative, got {qk_eps}")
+    f32, slots, nseqs = torch.float32, state_cache.shape[0], read_slot.shape[0]
+    if cu_seqlens is None and nseqs != tokens:
+        raise ValueError(f"{tokens} tokens of {nseqs} sequences need cu_seqlens")
+    cache = _whole(state_cache, "state_cache", device, f32, (slots, heads, dv, dk))
+    rs = _slots(read_slot, "read_slot", device, nseqs)
+    ws = _slots(write_slot, "write_slot", device, tokens)
+    cu = None if cu_seqlens is None else _slots(cu_seqlens, "cu_seqlens", device, nseqs + 1)
+    flag = _whole(error_flag, "error_flag", device, torch.int32, (1,))
+    row = heads * dv
+    args = (q.data_ptr(), _rows(q, "q", device, dtype, qshape, kheads * dk),
+            k.data_ptr(), _rows(k, "k", device, dtype, qshape, kheads * dk), v.data_ptr(),
+            _rows(v, "v", device, dtype, vshape, row), gate.data_ptr(),
+            _rows(gate, "gate", device, gate.dtype, (tokens, heads), heads), beta.data_ptr(),
+            _rows(beta, "beta", device, gate.dtype, (tokens, heads), heads),
+            _whole(A, "A", device, f32, (heads,)), _whole(dt_bias, "dt_bias", device, f32, (heads,)),
+            -1.0 if qk_eps is None else float(qk_eps), dk ** -0.5 if scale is None else float(scale))
+    o, o_stride = _out_rows(o, "o", v, row)
+    _enqueue("ssd_gated_delta_step", device, *args, code, code if gate.dtype == dtype else _dtype_code(gate), nseqs, tokens,
+             None if cu is None else cu.data_ptr(), heads, kheads, dk, dv, cache, slots, rs.data_ptr(), ws.data_ptr(),
+             o.data_ptr(), o_stride, flag)
+    return o
+
+
+@dataclasses.dataclass
+class StepTables:
+    """Device-resident maps of one step (see ssd_step_tables)."""
+    cu_seqlens: torch.Tensor    # (S+1,)
+    seq_lens: torch.Tensor      # (S,)
+    positions: torch.Tensor     # (T,)
+    token_seq: torch.Tensor     # (T,)
+    slots: torch.Tensor         # (T,)
+    read_slot: torch.Tensor     # (S,)
+    state_slot: torch.Tensor    # (T,)
+    free_count: Optional[torch.Tensor]   # (1,) blocks left
+    error_flag: torch.Tensor    # (1,)
+
+
+def step_tables(num_computed: torch.Tensor, num_new: torch.Tensor, block_table: torch.Tensor, block_size: int,
+                total_tokens: int, rows: Optional[torch.Tensor] = None, free_blocks: Optional[torch.Tensor] = None,
+                free_count: Optional[torch.Tensor] = None, free_count_out: Optional[torch.Tensor] = None,
+                num_blocks: Optional[int] = None, error_flag: Optional[torch.Tensor] = None) -> StepTables:
+    """ssd_step_tables: block tables and slot maps of one step. num_computed, num_new (S,): tokens of each request in
+    the caches and new in this step; total_tokens: their sum, or the padded batch's tokens. block_table int32 (table rows,
+    blocks) holds request s in row rows[s] (s without rows) and gets the new blocks, taken from the end of
+    free_blocks[:free_count]; what is left is written to free_count_out (a new tensor unless given; free_count itself
+    updates it in place). num_blocks bounds the table's entries (2^31 - 1 slots unless given)."""
+    device, i32 = block_table.device, torch.int32
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table must be (rows, blocks), got {tuple(block_table.shape)}")
+    if block_size < 1:
+        raise ValueError(f"block_size must be positive, got {block_size}")
+    nseqs, total_tokens = num_computed.shape[0], int(total_tokens)
+    if total_tokens < 0:
+        raise ValueError(f"total_tokens must not be negative, got {total_tokens}")
+    table_rows, width = block_table.shape
+    nc = _slots(num_computed, "num_computed", device, nseqs)
+    nn = _slots(num_new, "num_new", device, nseqs)
+    rw = None if rows is None else _slots(rows, "rows", device, nseqs)
+    table = _whole(block_table, "block_table", device, i32, (table_rows, width))
+    if free_blocks is None:
+        if free_count is not None or free_count_out is not None:
+            raise ValueError("free_count and free_count_out are given only with free_blocks")
+        free, nfree = None, 0
+    else:
+        if free_count is None:
+            raise ValueError("free_blocks needs free_count")
+        nfree = free_blocks.shape[0]
+        free = _whole(free_blocks, "free_blocks", device, i32, (nfree,))
+        if free_count_out is None:
+            free_count_out = torch.empty(1, dtype=i32, device=device)
+    count = _whole(free_count, "free_count", device, i32, (1,))
+    left = _whole(free_count_out, "free_count_out", device, i32, (1,))
+    if error_flag is None:
+        error_flag = torch.zeros(1, dtype=i32, device=device)
+    flag = _whole(error_flag, "error_flag", device, i32, (1,))
+    # one allocation for the maps; each starts on 16 bytes
+    s4, t4 = (nseqs + 4) & ~3, (total_tokens + 3) & ~3
+    maps = torch.empty(3 * s4 + 4 * t4, dtype=i32, device=device)
+    cu, lens, read = maps[:nseqs + 1], maps[s4:s4 + nseqs], maps[2 * s4:2 * s4 + nseqs]
+    pos, seq, slots, state = (maps[3 * s4 + i * t4:3 * s4 + i * t4 + total_tokens] for i in range(4))
+    if num_blocks is None:
+        num_blocks = 0x7fffffff // block_size
+    _enqueue("ssd_step_tables", device, nseqs, total_tokens, nc.data_ptr(), nn.data_ptr(),
+             None if rw is None else rw.data_ptr(), table, table_rows, width, int(block_size), int(num_blocks), free, nfree,
+             count, left, cu.data_ptr(), lens.data_ptr(), pos.data_ptr(), seq.data_ptr(), slots.data_ptr(),
+             read.data_ptr(), state.data_ptr(), flag)
+    return StepTables(cu, lens, pos, seq, slots, read, state, free_count_out, error_flag)
+
+
+def _paged(k_cache, v_cache, device, dtype):
+    """Checks a paged cache; returns (blocks, kv heads, block size, head dim)."""
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache must be (blocks, kv heads, block size, head dim), got {tuple(k_cache.shape)}")
+    blocks, heads, size, dim = k_cache.shape
+    _whole(k_cache, "k_cache", device, dtype, k_cache.shape)
+    _whole(v_cache, "v_cache", device, dtype, (blocks, heads, dim, size))
+    return blocks, heads, size, dim
+
+
+def kv_cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   slots: torch.Tensor, error_flag: Optional[torch.Tensor] = None):
+    """ssd_kv_cache_write: the keys and values of token t, k, v (T, kv heads, head dim) (rows may lie further apart), go to
+    slot slots[t] = block * block size + place of k_cache (blocks, kv heads, block size, head dim) and v_cache (blocks, kv
+    heads, head dim, block size); negative slots are skipped."""
+    device, dtype, shape = k.device, k.dtype, k.shape
+    blocks, heads, size, dim = _paged(k_cache, v_cache, device, dtype)
+    if len(shape) != 3 or shape[1:] != (heads, dim):
+        raise ValueError(f"k must be (tokens, {heads}, {dim}), got {tuple(shape)}")
+    to = _slots(slots, "slots", device, shape[0])
+    flag = _whole(error_flag, "error_flag", device, torch.int32, (1,))
+    row = heads * dim
+    _enqueue("ssd_kv_cache_write", device, k.data_ptr(), _rows(k, "k", device, dtype, shape, row), v.data_ptr(),
+             _rows(v, "v", device, dtype, shape, row), _dtype_code(k), shape[0], heads, dim, k_cache.data_ptr(),
+             v_cache.data_ptr(), blocks, size, to.data_ptr(), flag)
+
+
+@dataclasses.dataclass
+class AttentionPlan:
+    """How one step's attention is split (see ssd_attention_plan)."""
+    nseqs: int
+    total_tokens: int
+    max_new_tokens: int
+    window: int
+    max_parts: int
+    seq_lens: torch.Tensor
+    cu_seqlens: Optional[torch.Tensor]
+    part_start: torch.Tensor
+    part_seq: torch.Tensor
+    part_keys: torch.Tensor
+    error_flag: torch.Tensor
+
+    def c_struct(self) -> _Plan:
+        return _Plan(self.nseqs, self.total_tokens, self.max_new_tokens, self.window, self.max_parts,
+                     self.seq_lens.data_ptr(), None if self.cu_seqlens is None else self.cu_seqlens.data_ptr(),
+                     self.part_start.data_ptr(), self.part_seq.data_ptr(), self.part_keys.data_ptr(),
+                     self.error_flag.data_ptr())
+
+
+def attention_plan(seq_lens: torch.Tensor, num_heads: int, num_kv_heads: int, cu_seqlens: Optional[torch.Tensor] = None,
+                   total_tokens: Optional[int] = None, max_new_tokens: int = 1, window: int = 0) -> AttentionPlan:
+    """ssd_attention_plan_build: the split of one step's attention, for all layers with these heads and this window.
+    seq_lens (S,): keys of each sequence, its new tokens' among them. Without cu_seqlens every sequence has one new token;
+    with cu_seqlens (S+1,) pass total_tokens and max_new_tokens (the most of a sequence, up to 64)."""
+    device, i32 = seq_lens.device, torch.int32
+    if num_heads <= 0 or num_kv_heads <= 0 or num_heads % num_kv_heads:
+        raise ValueError(f"num_heads must be a multiple of num_kv_heads, got {num_heads} and {num_kv_heads}")
+    nseqs = seq_lens.shape[0]
+    if cu_seqlens is None:
+        if total_tokens not in (None, nseqs):
+            raise ValueError(f"{total_tokens} tokens of {nseqs} sequences need cu_seqlens")
+        total_tokens = nseqs
+    elif total_tokens is None:
+        raise ValueError("pass total_tokens with cu_seqlens")
+    lens = _slots(seq_lens, "seq_lens", device, nseqs)
+    cu = None if cu_seqlens is None else _slots(cu_seqlens, "cu_seqlens", device, nseqs + 1)
+    parts = nseqs + int((_lib or load_library()).ssd_paged_attention_parts(int(max_new_tokens), num_heads, num_kv_heads))
+    made = torch.zeros(nseqs + 3 + parts, dtype=i32, device=device)
+    plan = AttentionPlan(nseqs, int(total_tokens), int(max_new_tokens), int(window), parts, lens, cu, made[:nseqs + 1],
+                         made[nseqs + 3:], made[nseqs + 1:nseqs + 2], made[nseqs + 2:nseqs + 3])
+    _enqueue("ssd_attention_plan_build", device, ctypes.byref(plan.c_struct()))
+    return plan
+
+
+def paged_attention_step(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                         plan: AttentionPlan, rows: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                         out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, error_flag: Optional[torch.Tensor] = None):
+    """ssd_paged_attention_step: attention of the plan's new tokens, q (T, heads, head dim) (rows may lie further apart),
+    over the keys and values of their sequences in a paged cache (see kv_cache_write). block_table int32 (table rows,
+    blocks) holds sequence s in row rows[s] (s without rows). scale: head dim ** -0.5 unless given. lse (T, heads)
+    float32 receives the logarithms of the sums of exponentials. workspace (uint8, at least
+    paged_attention_workspace_size bytes) is allocated per call when not given. Returns out (T, heads, head dim)."""
+    device, dtype, shape = q.device, q.dtype, q.shape
+    blocks, kv_heads, size, dim = _paged(k_cache, v_cache, device, dtype)
+    if len(shape) != 3 or shape[0] != plan.total_tokens or shape[2] != dim:
+        raise ValueError(f"q must be ({plan.total_tokens}, heads, {dim}), got {tuple(shape)}")
+    if plan.part_start.device != device:
+        raise ValueError(f"the plan must be on {device}, got {plan.part_start.device}")
+    heads = shape[1]
+    if heads % kv_heads:
+        raise ValueError(f"q's heads must be a multiple of the cache's {kv_heads}, got {heads}")
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table must be (rows, blocks), got {tuple(block_table.shape)}")
+    table_rows, width = block_table.shape
+    table = _whole(block_table, "block_table", device, torch.int32, (table_rows, width))
+    if rows is None and table_rows < plan.nseqs:
+        raise ValueError(f"block_table must have {plan.nseqs} rows, got {table_rows}")
+    rw = None if rows is None else _slots(rows, "rows", device, plan.nseqs)
+    flag = _whole(error_flag, "error_flag", device, torch.int32, (1,))
+    q_stride = _rows(q, "q", device, dtype, shape, heads * dim)
+    log = _whole(lse, "lse", device, torch.float32, (shape[0], heads))
+    need = paged_attention_workspace_size(plan, heads, dim)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    ws = _whole(workspace, "workspace", device, torch.uint8, (workspace.numel(),))
+    out, out_stride = _out_rows(out, "out", q, heads * dim)
+    _enqueue("ssd_paged_attention_step", device, q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(),
+             _dtype_code(q), dim ** -0.5 if scale is None else float(scale), ctypes.byref(plan.c_struct()), heads, kv_heads,
+             dim, table, table_rows, width, None if rw is None else rw.data_ptr(), blocks, size, out.data_ptr(), out_stride,
+             log, ws, workspace.numel(), flag)
+    return out
+
+
+def paged_attention_workspace_size(plan: AttentionPlan, num_heads: int, head_dim: int) -> int:
+    """Bytes of device workspace that paged_attention_step needs for this plan."""
+    return int((_lib or load_library()).ssd_paged_attention_workspace_size(plan.max_parts, plan.max_new_tokens,
+                                                                            int(num_heads), int(head_dim)))
+
+
+def _add_norm_inputs(x, weight, residual, residual_out):
+    """Checks what the two norms with a residual share; returns the library's leading arguments, the residual's output
+    and the rest of the arguments that describe it."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be (rows, channels), got {tuple(x.shape)}")
+    device, dtype, shape = x.device, x.dtype, x.shape
+    channels = shape[1]
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out is given only with residual")
+    head = (x.data_ptr(), _rows(x, "x", device, dtype, shape, channels),
+            None if residual is None else residual.data_ptr(),
+            0 if residual is None else _rows(residual, "residual", device, dtype, shape, channels),
+            _whole(weight, "weight", device, torch.float32, (channels,)), _dtype_code(x), shape[0], channels)
+    if residual is None:
+        return head, None, (None, 0)
+    residual_out, stride = _out_rows(residual_out, "residual_out", x, channels)
+    return head, residual_out, (residual_out.data_ptr(), stride)
+
+
+def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, residual_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """ssd_add_rms_norm: r = x + residual, out = r / sqrt(mean(r^2) + eps) * weight, over the rows of x (rows, channels)
+    (which may lie further apart). residual_out receives r (a new tensor unless given; residual itself updates it in
+    place). Returns (out, residual_out), the latter None without residual."""
+    head, residual_out, res = _add_norm_inputs(x, weight, residual, residual_out)
+    out, out_stride = _out_rows(out, "out", x, x.shape[1])
+    _enqueue("ssd_add_rms_norm", x.device, *head, float(eps), *res, out.data_ptr(), out_stride)
+    return out, residual_out
+
+
+def add_rms_norm_e4m3(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                      eps: float = 1e-6, group: int = 0, scale: Optional[torch.Tensor] = None,
+                      residual_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      scales: Optional[torch.Tensor] = None):
+    """ssd_add_rms_norm_e4m3: add_rms_norm with its result in 8 bits, out = e4m3(norm / scale) as float8_e4m3fn. `scale`
+    (1,) is used as given; without it every `group` channels (0: a whole row) get the scale max |norm| / 448 (1 where all
+    are zero). Returns (out, scales (rows, channels / group) or the given scale, residual_out or None)."""
+    head, residual_out, res = _add_norm_inputs(x, weight, residual, residual_out)
+    device, (rows, channels), f32 = x.device, x.shape, torch.float32
+    group = int(group) or channels
+    if group < 0 or channels % max(group, 1):
+        raise ValueError(f"group must divide the {channels} channels, got {group}")
+    if scale is not None and scales is not None:
+        raise ValueError("scales is written only without a given scale")
+    given = _whole(scale, "scale", device, f32, (1,))
+    if scale is None and scales is None:
+        scales = torch.empty(rows, channels // max(group, 1), dtype=f32, device=device)
+    made = None if scales is None else _whole(scales, "scales", device, f32, (rows, channels // group))
+    if out is None:
+        out = torch.empty(rows, channels, dtype=torch.float8_e4m3fn, device=device)
+    out_stride = _rows(out, "out", device, torch.float8_e4m3fn, x.shape, channels)
+    _enqueue("ssd_add_rms_norm_e4m3", device, *head, group, float(eps), given, made, *res, out.data_ptr(), out_stride)
+    return out, scales if scale is None else scale, residual_out
