@@ -382,7 +382,8 @@ __global__ __launch_bounds__(256) void ssd_attention_join_kernel(AttnArgs a) {
     if (a.lse != nullptr && d == 0) a.lse[(int64_t)t * a.Hq + head] = (best + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
 }
 
-// Copies the rows of new tokens to their slots: keys as they are, values turned.
+// Copies the rows of new tokens to their slots: keys as they are, values turned. One token and 16 bytes of its row a lane:
+// for few tokens, whose slots lie apart anyway.
 template <typename T>
 __global__ __launch_bounds__(256) void ssd_kv_write_kernel(KvWriteArgs a) {
     constexpr int W = 16 / sizeof(T);
@@ -405,6 +406,68 @@ __global__ __launch_bounds__(256) void ssd_kv_write_kernel(KvWriteArgs a) {
     T *vc = reinterpret_cast<T *>(a.v_cache) + head + (int64_t)d * a.block + at;
 #pragma unroll
     for (int j = 0; j < W; ++j) vc[(int64_t)j * a.block] = v[j];
+}
+
+// The same for many tokens: 64 tokens of one head a workgroup, the values turned in LDS, so that a store's lanes are
+// tokens, whose places in a prompt's block follow each other: a store writes whole lines of the values (single values
+// scattered took 7 times as long).
+template <typename T, int D>
+__global__ __launch_bounds__(256) void ssd_kv_write_tile_kernel(KvWriteArgs a) {
+    constexpr int W = 16 / sizeof(T), PER = D / W, ROW = D * sizeof(T) + 8;   // 16-byte pieces of a row; its bytes in LDS
+    constexpr int ROUNDS = 64 * PER / 256, WORDS = D * sizeof(T) / 4;
+    __shared__ __attribute__((aligned(16))) char tile[64 * ROW];
+    __shared__ int slots[64];
+    const int h = blockIdx.x % a.Hkv;
+    const int64_t t0 = (int64_t)(blockIdx.x / a.Hkv) * 64;
+    if (threadIdx.x < 64) {
+        int slot = t0 + threadIdx.x < a.T ? a.slots[t0 + threadIdx.x] : -1;
+        if (slot >= a.num_slots) {
+            if (h == 0 && a.error_flag != nullptr) atomicOr(a.error_flag, SSD_DATA_BAD_SLOT);
+            slot = -1;
+        }
+        slots[threadIdx.x] = slot;
+    }
+    Raw16<T> k[ROUNDS], v[ROUNDS];
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const int i = r * 256 + threadIdx.x;
+        const int64_t t = t0 + i / PER, e = (int64_t)h * D + i % PER * W;
+        if (t < a.T) {
+            k[r] = *reinterpret_cast<const Raw16<T> *>(reinterpret_cast<const T *>(a.k) + t * a.k_stride + e);
+            v[r] = *reinterpret_cast<const Raw16<T> *>(reinterpret_cast<const T *>(a.v) + t * a.v_stride + e);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const int i = r * 256 + threadIdx.x;
+        u32x2 *to = reinterpret_cast<u32x2 *>(tile + i / PER * ROW + i % PER * 16);
+        to[0] = u32x2{v[r].w[0], v[r].w[1]};
+        to[1] = u32x2{v[r].w[2], v[r].w[3]};
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const int i = r * 256 + threadIdx.x, slot = slots[i / PER];
+        if (slot < 0) continue;
+        const int block = slot / a.block, at = slot - block * a.block;
+        T *to = reinterpret_cast<T *>(a.k_cache) + (((int64_t)block * a.Hkv + h) * a.block + at) * D + i % PER * W;
+        *reinterpret_cast<u32x4 *>(to) = u32x4{k[r].w[0], k[r].w[1], k[r].w[2], k[r].w[3]};
+    }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, slot = slots[lane];
+    if (slot < 0) return;
+    const int block = slot / a.block, at = slot - block * a.block;
+    T *to = reinterpret_cast<T *>(a.v_cache) + ((int64_t)block * a.Hkv + h) * a.block * D + at;
+#pragma unroll 8
+    for (int w = wave; w < WORDS; w += 4) {
+        const uint32_t word = *reinterpret_cast<const uint32_t *>(tile + lane * ROW + 4 * w);
+        if constexpr (sizeof(T) == 4) {
+            to[(int64_t)w * a.block] = __uint_as_float(word);
+        } else {
+            uint16_t *at2 = reinterpret_cast<uint16_t *>(to) + (int64_t)2 * w * a.block;
+            at2[0] = (uint16_t)word;
+            at2[a.block] = (uint16_t)(word >> 16);
+        }
+    }
 }
 
 template <typename T, int D> hipError_t launch_attention_d(const AttnArgs &a, hipStream_t stream) {
@@ -437,13 +500,24 @@ hipError_t launch_attention(const AttnArgs &a, bool bf16, int D, hipStream_t str
     return bf16 ? launch_attention_t<__bf16>(a, D, stream) : launch_attention_t<float>(a, D, stream);
 }
 
-hipError_t launch_kv_write(const KvWriteArgs &a, bool bf16, hipStream_t stream) {
-    const int64_t lanes = (int64_t)a.T * a.Hkv * a.D / (bf16 ? 8 : 4);
-    const int64_t blocks = (lanes + 255) / 256;
+// From this many tokens on the values are turned in LDS.
+constexpr int kTileTokens = 1024;
+
+template <typename T> static hipError_t launch_kv_write_t(const KvWriteArgs &a, hipStream_t stream) {
+    const bool tiles = a.T >= kTileTokens;
+    const int64_t lanes = (int64_t)a.T * a.Hkv * a.D * sizeof(T) / 16;
+    const int64_t blocks = tiles ? ((int64_t)a.T + 63) / 64 * a.Hkv : (lanes + 255) / 256;
     if (!fits_grid(blocks, 256)) return hipErrorInvalidConfiguration;
-    if (bf16) hipLaunchKernelGGL((ssd_kv_write_kernel<__bf16>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((ssd_kv_write_kernel<float>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+    const dim3 grid((unsigned)blocks), block(256);
+    if (!tiles) hipLaunchKernelGGL((ssd_kv_write_kernel<T>), grid, block, 0, stream, a);
+    else if (a.D == 64) hipLaunchKernelGGL((ssd_kv_write_tile_kernel<T, 64>), grid, block, 0, stream, a);
+    else if (a.D == 128) hipLaunchKernelGGL((ssd_kv_write_tile_kernel<T, 128>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((ssd_kv_write_tile_kernel<T, 256>), grid, block, 0, stream, a);
     return hipGetLastError();
+}
+
+hipError_t launch_kv_write(const KvWriteArgs &a, bool bf16, hipStream_t stream) {
+    return bf16 ? launch_kv_write_t<__bf16>(a, stream) : launch_kv_write_t<float>(a, stream);
 }
 
 }  // namespace ssd
