@@ -6,8 +6,10 @@
 // The norm takes r before its rounding to residual_out.
 //
 // Memory-bound: x, the residual and the outputs pass once; a row stays in the
-// registers of one workgroup (lane l holds vectors l, l + THREADS, ..) between
+// registers of its team of lanes (lane l holds vectors l, l + TEAM, ..) between
 // the loads, the sum of squares, the maxima and the stores.
+#include <algorithm>
+
 #include "ssd_norm.hpp"
 
 namespace ssd {
@@ -16,125 +18,216 @@ constexpr float kE4m3Max = 448.0f;
 
 // e4m3 of four values, clamped to the largest (NaN stays NaN).
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
-    auto clamp = [](float v) { return v != v ? v : fminf(fmaxf(v, -kE4m3Max), kE4m3Max); };
+    auto clamp = [](float v) { return v != v ? v : __builtin_amdgcn_fmed3f(v, -kE4m3Max, kE4m3Max); };
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp(a), clamp(b), 0, false);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(clamp(c), clamp(d), w, true);
 }
 
-template <typename T, int THREADS, int V, int R, bool Q>
-__global__ __launch_bounds__(THREADS) void ssd_add_rms_norm_kernel(AddNormArgs a) {
+// Largest of `lanes` neighbouring lanes (a power of two up to 64, uniform); every lane gets it.
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v, int lanes) {
+    auto dpp = [&](auto ctrl) {
+        v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    if (lanes > 1) dpp(std::integral_constant<int, 0xB1>{});    // lane ^ 1
+    if (lanes > 2) dpp(std::integral_constant<int, 0x4E>{});    // lane ^ 2
+    if (lanes > 4) dpp(std::integral_constant<int, 0x141>{});   // 7 - lane of 8
+    if (lanes > 8) dpp(std::integral_constant<int, 0x140>{});   // 15 - lane of 16
+    if (lanes > 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = max(r[0], r[1]);
+    }
+    if (lanes > 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = max(r[0], r[1]);
+    }
+    return v;
+}
+
+// Where a row's scales come from: none (no 8 bits), a given one, the whole row, groups inside a wave's lanes, larger groups.
+enum Scales { kNoScale, kGiven, kRowScale, kLaneGroups, kWideGroups };
+
+template <typename T, int TEAM, int V, int R, Scales Q>
+__global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void ssd_add_rms_norm_kernel(AddNormArgs a) {
     using IO = NormIO<T, V>;
     using Raw = typename IO::Raw;
-    constexpr int SPAN = THREADS * V;
-    __shared__ float part[THREADS / 64];
-    __shared__ uint32_t top[Q ? kNormMaxGroup / 32 : 1];   // bits of the groups' largest absolute values
-    const int tid = threadIdx.x, C = a.channels;
-    const int64_t row = blockIdx.x;
-    const T *x = reinterpret_cast<const T *>(a.x) + row * a.x_stride;
-    const T *res = a.residual ? reinterpret_cast<const T *>(a.residual) + row * a.residual_stride : nullptr;
-    T *res_out = a.residual_out ? reinterpret_cast<T *>(a.residual_out) + row * a.residual_out_stride : nullptr;
-    auto at = [&](int r) { return r * SPAN + tid * V; };
+    struct __attribute__((packed, aligned(4))) Weights { float w[V]; };
+    constexpr int THREADS = TEAM > 256 ? TEAM : 256, SPAN = TEAM * V;
+    __shared__ float part[TEAM > 64 ? TEAM / 64 : 1];
+    constexpr int TOPS = Q == kWideGroups ? TEAM * 16 / 128 : TEAM / 64;   // (wide groups have 128 channels at least)
+    __shared__ uint32_t tops[Q == kWideGroups || Q == kRowScale ? THREADS / TEAM * TOPS : 1];
+    const int lane = threadIdx.x % TEAM, C = a.channels;
+    uint32_t *top = tops + (Q == kWideGroups || Q == kRowScale ? threadIdx.x / TEAM * TOPS : 0);
+    auto team_sync = [] {   // a wave's LDS operations are in order by themselves
+        if constexpr (TEAM > 64) __syncthreads();
+        else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    };
+    const int64_t row = (int64_t)blockIdx.x * (THREADS / TEAM) + threadIdx.x / TEAM;
+    if (row >= a.rows) return;   // (whole waves; a team of more than a wave is a workgroup)
+    const T *x = reinterpret_cast<const T *>(a.x) + row * a.x_stride + lane * V;
+    const T *res = reinterpret_cast<const T *>(a.residual) + row * a.residual_stride + lane * V;
+    T *res_out = reinterpret_cast<T *>(a.residual_out) + row * a.residual_out_stride + lane * V;
+    auto live = [&](int r) { return r * SPAN + lane * V < C; };
     Raw rx[R], rr[R];
+    Weights w[R];
 #pragma unroll
     for (int r = 0; r < R; ++r)
-        if (at(r) < C) {
-            rx[r] = *reinterpret_cast<const Raw *>(x + at(r));
-            if (res) rr[r] = *reinterpret_cast<const Raw *>(res + at(r));
+        if (live(r)) {
+            rx[r] = *reinterpret_cast<const Raw *>(x + r * SPAN);
+            if (a.residual) rr[r] = *reinterpret_cast<const Raw *>(res + r * SPAN);
         }
-    if constexpr (Q)
-        if (a.scale == nullptr)
-            for (int i = tid; i < C / a.group; i += THREADS) top[i] = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (live(r)) {
+            if (a.weight) w[r] = *reinterpret_cast<const Weights *>(a.weight + r * SPAN + lane * V);
+            else
+#pragma unroll
+                for (int i = 0; i < V; ++i) w[r].w[i] = 1.0f;
+        }
+    if constexpr (Q == kWideGroups) {
+        for (int i = lane; i < C / a.group; i += TEAM) top[i] = 0;
+        team_sync();
+    }
     float v[R * V], sq = 0.0f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[r * V + i] = 0.0f;
-        if (at(r) >= C) continue;
+        if (!live(r)) continue;
         IO::unpack(rx[r], v + r * V);
-        if (res) {
+        if (a.residual) {
             float y[V];
             IO::unpack(rr[r], y);
 #pragma unroll
             for (int i = 0; i < V; ++i) v[r * V + i] += y[i];
         }
-        if (res_out) *reinterpret_cast<Raw *>(res_out + at(r)) = IO::pack(v + r * V);
+        if (a.residual_out) *reinterpret_cast<Raw *>(res_out + r * SPAN) = IO::pack(v + r * V);
 #pragma unroll
         for (int i = 0; i < V; ++i) sq = fmaf(v[r * V + i], v[r * V + i], sq);
     }
-    const float inv = 1.0f / sqrtf(team_sum<THREADS>(sq, part) / (float)C + a.eps);
+    const float inv = 1.0f / sqrtf(team_sum<TEAM>(sq, part) / (float)C + a.eps);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        if (at(r) >= C) continue;
+        if (!live(r)) continue;
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[r * V + i] *= inv * (a.weight ? a.weight[at(r) + i] : 1.0f);
-        if constexpr (!Q) *reinterpret_cast<Raw *>(reinterpret_cast<T *>(a.out) + row * a.out_stride + at(r)) = IO::pack(v + r * V);
+        for (int i = 0; i < V; ++i) v[r * V + i] *= inv * w[r].w[i];
+        if constexpr (Q == kNoScale)
+            *reinterpret_cast<Raw *>(reinterpret_cast<T *>(a.out) + row * a.out_stride + r * SPAN + lane * V) = IO::pack(v + r * V);
     }
-    if constexpr (Q) {
-        uint8_t *out = reinterpret_cast<uint8_t *>(a.out) + row * a.out_stride;
-        if (a.scale == nullptr) {
-            // (absolute values compare as their bits do, a NaN above all)
-            __syncthreads();
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                if (at(r) >= C) continue;
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < V; ++i) m = max(m, __float_as_uint(v[r * V + i]) & 0x7fffffffu);
-                atomicMax(&top[at(r) / a.group], m);
-            }
-            __syncthreads();
-            for (int i = tid; i < C / a.group; i += THREADS) {
-                const float t = __uint_as_float(top[i]);
-                a.scales[row * (C / a.group) + i] = t == 0.0f ? 1.0f : t / kE4m3Max;
-            }
-        }
+    if constexpr (Q != kNoScale) {
+        // (absolute values compare as their bits do, a NaN above all)
+        uint32_t m[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (at(r) >= C) continue;
-            float s;
-            if (a.scale != nullptr) {
-                s = *a.scale;
-            } else {
-                const float t = __uint_as_float(top[at(r) / a.group]);
-                s = t == 0.0f ? 1.0f : t / kE4m3Max;
+            m[r] = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) m[r] = max(m[r], __float_as_uint(v[r * V + i]) & 0x7fffffffu);
+        }
+        auto scale_of = [](uint32_t bits) { return bits == 0 ? 1.0f : __uint_as_float(bits) * (1.0f / kE4m3Max); };
+        float scale[R];
+        if constexpr (Q == kGiven) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) scale[r] = *a.scale;
+        } else if constexpr (Q == kRowScale) {
+            uint32_t all = 0;
+#pragma unroll
+            for (int r = 0; r < R; ++r) all = max(all, m[r]);
+            all = lanes_max(all, 64);
+            if constexpr (TEAM > 64) {
+                if ((lane & 63) == 0) top[lane >> 6] = all;
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < TEAM / 64; ++k) all = max(all, top[k]);
             }
-            if constexpr (V >= 4) {
 #pragma unroll
-                for (int i = 0; i < V; i += 4)
-                    *reinterpret_cast<uint32_t *>(out + at(r) + i) =
-                        pack_e4m3(v[r * V + i] / s, v[r * V + i + 1] / s, v[r * V + i + 2] / s, v[r * V + i + 3] / s);
+            for (int r = 0; r < R; ++r) scale[r] = scale_of(all);
+            if (lane == 0) a.scales[row] = scale[0];
+        } else if constexpr (Q == kLaneGroups) {
+            const int lanes = a.group / V;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                scale[r] = scale_of(lanes_max(m[r], lanes));
+                if (live(r) && (lane & (lanes - 1)) == 0)
+                    a.scales[row * (C / a.group) + (r * SPAN + lane * V) / a.group] = scale[r];
+            }
+        } else {   // a group spans several waves
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint32_t most = lanes_max(m[r], 64);
+                if (live(r) && (lane & 63) == 0) atomicMax(&top[(r * SPAN + lane * V) / a.group], most);
+            }
+            team_sync();
+            for (int i = lane; i < C / a.group; i += TEAM) a.scales[row * (C / a.group) + i] = scale_of(top[i]);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (live(r)) scale[r] = scale_of(top[(r * SPAN + lane * V) / a.group]);
+        }
+        uint8_t *out = reinterpret_cast<uint8_t *>(a.out) + row * a.out_stride + lane * V;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (!live(r)) continue;
+            float *f = v + r * V;
+            if (scale[r] < 0x1p-100f) {   // whose reciprocal may be infinite
+                scale[r] *= 0x1p100f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) f[i] *= 0x1p100f;
+            }
+            const float per = 1.0f / scale[r];
+            if constexpr (V == 8) {
+                *reinterpret_cast<u32x2 *>(out + r * SPAN) = u32x2{pack_e4m3(f[0] * per, f[1] * per, f[2] * per, f[3] * per),
+                                                                   pack_e4m3(f[4] * per, f[5] * per, f[6] * per, f[7] * per)};
+            } else if constexpr (V == 4) {
+                *reinterpret_cast<uint32_t *>(out + r * SPAN) = pack_e4m3(f[0] * per, f[1] * per, f[2] * per, f[3] * per);
             } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i) out[at(r) + i] = (uint8_t)pack_e4m3(v[r * V + i] / s, 0.0f, 0.0f, 0.0f);
+                for (int i = 0; i < V; ++i) out[r * SPAN + i] = (uint8_t)pack_e4m3(f[i] * per, 0.0f, 0.0f, 0.0f);
             }
         }
     }
 }
 
-template <typename T, int THREADS, int V, bool Q> static hipError_t launch_addnorm_threads(const AddNormArgs &a, hipStream_t stream) {
-    hipLaunchKernelGGL((ssd_add_rms_norm_kernel<T, THREADS, V, 16 / V, Q>), dim3((unsigned)a.rows), dim3(THREADS), 0, stream, a);
+template <typename T, int TEAM, int V, Scales Q> static hipError_t launch_addnorm_team(const AddNormArgs &a, hipStream_t stream) {
+    constexpr int THREADS = TEAM > 256 ? TEAM : 256, ROWS = THREADS / TEAM;
+    const int64_t blocks = ((int64_t)a.rows + ROWS - 1) / ROWS;
+    if (!fits_grid(blocks, THREADS)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((ssd_add_rms_norm_kernel<T, TEAM, V, 16 / V, Q>), dim3((unsigned)blocks), dim3(THREADS), 0, stream, a);
     return hipGetLastError();
 }
 
-template <typename T, int V, bool Q> static hipError_t launch_addnorm_v(const AddNormArgs &a, hipStream_t stream) {
-    if (a.channels <= 256 * 16) return launch_addnorm_threads<T, 256, V, Q>(a, stream);
-    return launch_addnorm_threads<T, 1024, V, Q>(a, stream);
+// The smallest team that holds a row with 16 values a lane.
+template <typename T, int V, Scales Q, int TEAM = 64> static hipError_t launch_addnorm_size(const AddNormArgs &a, hipStream_t stream) {
+    if constexpr (TEAM < 1024) {
+        if (a.channels <= TEAM * 16) return launch_addnorm_team<T, TEAM, V, Q>(a, stream);
+        return launch_addnorm_size<T, V, Q, TEAM == 64 ? 256 : 2 * TEAM>(a, stream);
+    } else {
+        static_assert(1024 * 16 >= kNormMaxGroup, "the largest team holds the largest row");
+        return launch_addnorm_team<T, 1024, V, Q>(a, stream);
+    }
 }
 
-template <typename T, bool Q> static hipError_t launch_addnorm_t(const AddNormArgs &a, hipStream_t stream) {
+template <typename T, int V> static hipError_t launch_addnorm_v(const AddNormArgs &a, bool e4m3, hipStream_t stream) {
+    if (!e4m3) return launch_addnorm_size<T, V, kNoScale>(a, stream);
+    if (a.scale != nullptr) return launch_addnorm_size<T, V, kGiven>(a, stream);
+    if (a.group == a.channels) return launch_addnorm_size<T, V, kRowScale>(a, stream);
+    if constexpr (V < 8)   // (groups have 512 channels at most)
+        if (a.group > 64 * V) return launch_addnorm_size<T, V, kWideGroups>(a, stream);
+    return launch_addnorm_size<T, V, kLaneGroups>(a, stream);
+}
+
+// Vectors of 16 bytes where all rows start on such, single values elsewhere.
+template <typename T> static hipError_t launch_addnorm_t(const AddNormArgs &a, bool e4m3, hipStream_t stream) {
     const uint64_t rows = (uint64_t)(a.x_stride | (a.residual ? a.residual_stride : 0) |
-                                     (a.residual_out ? a.residual_out_stride : 0) | (Q ? 0 : a.out_stride) | a.channels);
+                                     (a.residual_out ? a.residual_out_stride : 0) | (e4m3 ? 0 : a.out_stride) | a.channels);
     const uint64_t starts = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.residual) |
-                            reinterpret_cast<uintptr_t>(a.residual_out) | (Q ? 0 : reinterpret_cast<uintptr_t>(a.out)) |
+                            reinterpret_cast<uintptr_t>(a.residual_out) | (e4m3 ? 0 : reinterpret_cast<uintptr_t>(a.out)) |
                             rows * sizeof(T);
-    const uint64_t codes = Q ? reinterpret_cast<uintptr_t>(a.out) | (uint64_t)a.out_stride : 0;   // whole words of 8-bit values
-    if (starts % 16 == 0 && codes % 4 == 0) return launch_addnorm_v<T, 16 / sizeof(T), Q>(a, stream);
-    return launch_addnorm_v<T, 1, Q>(a, stream);
+    constexpr int V = 16 / sizeof(T);
+    const uint64_t codes = e4m3 ? reinterpret_cast<uintptr_t>(a.out) | (uint64_t)a.out_stride : 0;   // V 8-bit values at a time
+    if (starts % 16 == 0 && codes % V == 0) return launch_addnorm_v<T, V>(a, e4m3, stream);
+    return launch_addnorm_v<T, 1>(a, e4m3, stream);
 }
 
 hipError_t launch_add_rms_norm(const AddNormArgs &a, bool bf16, bool e4m3, hipStream_t stream) {
-    if (bf16) return e4m3 ? launch_addnorm_t<__bf16, true>(a, stream) : launch_addnorm_t<__bf16, false>(a, stream);
-    return e4m3 ? launch_addnorm_t<float, true>(a, stream) : launch_addnorm_t<float, false>(a, stream);
+    return bf16 ? launch_addnorm_t<__bf16>(a, e4m3, stream) : launch_addnorm_t<float>(a, e4m3, stream);
 }
 
 }  // namespace ssd

@@ -111,6 +111,24 @@ def test_values_far_from_one():
         ref.check(out, norm, ref.rounded(norm, norm.abs() * rel + 1e-45, F32), f"scale {scale}")
 
 
+def test_8_bit_output_of_values_near_the_smallest():
+    """Scales whose reciprocals are past float32's largest."""
+    x = torch.randn(3, 256, generator=torch.Generator().manual_seed(6)).cuda()
+    x[:, 5] = 0
+    w = torch.full((256,), 1e-37, device="cuda")
+    code, scales, _ = ssd.add_rms_norm_e4m3(x, weight=w, group=64)
+    torch.cuda.synchronize()
+    _, norm, rel = ref.add_rms_norm(x, None, w, 1e-6)
+    assert (scales < 2.0 ** -126).all() and (code[:, 5].float() == 0).all()
+    wide = scales.double().cpu().repeat_interleave(64, 1)
+    y = norm / wide
+    # scales and norms of this size are off by up to 2^-149, the smallest step; codes by that, and by half a step
+    top = norm.view(3, -1, 64).abs().amax(-1)
+    ref.check(scales, top / 448, torch.full_like(top, 2.0 ** -149) + top / 448 * (rel + 3 * ref.EPS), "scales")
+    err = y.abs() * (rel + 3 * ref.EPS) + 2.0 ** -149 / wide
+    ref.check(code.float(), y.clamp(-448, 448), torch.maximum((y.abs() + err) * 2.0 ** -4, torch.full_like(y, 2.0 ** -10)) + err, "codes")
+
+
 def test_in_place_and_beside_other_columns():
     i = inputs(20, 96, BF, seed=5)
     want, want_res = ssd.add_rms_norm(i["x"], weight=i["weight"], residual=i["residual"])
