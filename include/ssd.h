@@ -602,8 +602,8 @@ ssd_status ssd_gated_delta_step(
  *  free_blocks     int32 (num_free) or NULL; free_count int32 [1], at most
  *                  num_free; free_count_out int32 [1], may be free_count itself
  *                  (both may be NULL when free_blocks is NULL)
- * All pointers are device pointers. One launch for up to 4096 tokens, two
- * beyond. nseqs, total_tokens and max_blocks up to 2^20, num_free up to 2^29,
+ * All pointers are device pointers. One launch for up to 4096 tokens of up
+ * to 1024 requests, two beyond. nseqs, total_tokens and max_blocks up to 2^20, num_free up to 2^29,
  * num_blocks * block_size up to 2^31 - 1.
  * Errors: SSD_ERR_NULL_ARG, SSD_ERR_SHAPE (sizes outside these),
  * SSD_ERR_BLOCK_SIZE (block_size < 1), SSD_ERR_HIP.

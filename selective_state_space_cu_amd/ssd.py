@@ -543,6 +543,9 @@ def _rows(t: torch.Tensor, name: str, device, dtype, shape, row: int) -> int:
         raise ValueError(f"{name} has {shape[0]} rows, more than 2^31 - 1")
     if t.is_contiguous():
         return row
+    stride = t.stride()
+    if stride[-1] == 1 and shape[0] > 1 and (len(shape) == 2 or len(shape) == 3 and stride[1] == shape[2]):
+        return stride[0]
     step = 1
     for size, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
         if size != 1 and stride != step:
@@ -739,12 +742,12 @@ def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gate: to
     ws = _slots(write_slot, "write_slot", device, tokens)
     cu = None if cu_seqlens is None else _slots(cu_seqlens, "cu_seqlens", device, nseqs + 1)
     flag = _whole(error_flag, "error_flag", device, torch.int32, (1,))
-    row = heads * dv
-    args = (q.data_ptr(), _rows(q, "q", device, dtype, qshape, kheads * dk),
-            k.data_ptr(), _rows(k, "k", device, dtype, qshape, kheads * dk), v.data_ptr(),
+    row, keys, gshape, gtype = heads * dv, kheads * dk, (tokens, heads), gate.dtype
+    args = (q.data_ptr(), _rows(q, "q", device, dtype, qshape, keys),
+            k.data_ptr(), _rows(k, "k", device, dtype, qshape, keys), v.data_ptr(),
             _rows(v, "v", device, dtype, vshape, row), gate.data_ptr(),
-            _rows(gate, "gate", device, gate.dtype, (tokens, heads), heads), beta.data_ptr(),
-            _rows(beta, "beta", device, gate.dtype, (tokens, heads), heads),
+            _rows(gate, "gate", device, gtype, gshape, heads), beta.data_ptr(),
+            _rows(beta, "beta", device, gtype, gshape, heads),
             _whole(A, "A", device, f32, (heads,)), _whole(dt_bias, "dt_bias", device, f32, (heads,)),
             -1.0 if qk_eps is None else float(qk_eps), dk ** -0.5 if scale is None else float(scale))
     o, o_stride = _out_rows(o, "o", v, row)
@@ -765,7 +768,6 @@ class StepTables:
     read_slot: torch.Tensor     # (S,)
     state_slot: torch.Tensor    # (T,)
     free_count: Optional[torch.Tensor]   # (1,) blocks left
-    error_flag: torch.Tensor    # (1,)
 
 
 def step_tables(num_computed: torch.Tensor, num_new: torch.Tensor, block_table: torch.Tensor, block_size: int,
@@ -803,21 +805,22 @@ def step_tables(num_computed: torch.Tensor, num_new: torch.Tensor, block_table: 
             free_count_out = torch.empty(1, dtype=i32, device=device)
     count = _whole(free_count, "free_count", device, i32, (1,))
     left = _whole(free_count_out, "free_count_out", device, i32, (1,))
-    if error_flag is None:
-        error_flag = torch.zeros(1, dtype=i32, device=device)
     flag = _whole(error_flag, "error_flag", device, i32, (1,))
-    # one allocation for the maps; each starts on 16 bytes
-    s4, t4 = (nseqs + 4) & ~3, (total_tokens + 3) & ~3
-    maps = torch.empty(3 * s4 + 4 * t4, dtype=i32, device=device)
-    cu, lens, read = maps[:nseqs + 1], maps[s4:s4 + nseqs], maps[2 * s4:2 * s4 + nseqs]
-    pos, seq, slots, state = (maps[3 * s4 + i * t4:3 * s4 + i * t4 + total_tokens] for i in range(4))
+    # one allocation for the maps
+    maps = torch.empty(3 * nseqs + 1 + 4 * total_tokens, dtype=i32, device=device)
+    parts = maps.split_with_sizes((nseqs + 1, nseqs, nseqs, total_tokens, total_tokens, total_tokens, total_tokens))
+    cu = maps.data_ptr()
+    lens = cu + 4 * (nseqs + 1)
+    read = lens + 4 * nseqs
+    pos = read + 4 * nseqs
+    one = 4 * total_tokens
     if num_blocks is None:
         num_blocks = 0x7fffffff // block_size
     _enqueue("ssd_step_tables", device, nseqs, total_tokens, nc.data_ptr(), nn.data_ptr(),
              None if rw is None else rw.data_ptr(), table, table_rows, width, int(block_size), int(num_blocks), free, nfree,
-             count, left, cu.data_ptr(), lens.data_ptr(), pos.data_ptr(), seq.data_ptr(), slots.data_ptr(),
-             read.data_ptr(), state.data_ptr(), flag)
-    return StepTables(cu, lens, pos, seq, slots, read, state, free_count_out, error_flag)
+             count, left, cu, lens, pos, pos + one, pos + 2 * one, read, pos + 3 * one, flag)
+    cu, lens, read, pos, seq, slots, state = parts
+    return StepTables(cu, lens, pos, seq, slots, read, state, free_count_out)
 
 
 def _paged(k_cache, v_cache, device, dtype):
@@ -847,7 +850,7 @@ def kv_cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
              v_cache.data_ptr(), blocks, size, to.data_ptr(), flag)
 
 
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True)
 class AttentionPlan:
     """How one step's attention is split (see ssd_attention_plan)."""
     nseqs: int
@@ -862,11 +865,17 @@ class AttentionPlan:
     part_keys: torch.Tensor
     error_flag: torch.Tensor
 
+    def __post_init__(self):
+        # what every layer's call passes is made once
+        c = _Plan(self.nseqs, self.total_tokens, self.max_new_tokens, self.window, self.max_parts,
+                  self.seq_lens.data_ptr(), None if self.cu_seqlens is None else self.cu_seqlens.data_ptr(),
+                  self.part_start.data_ptr(), self.part_seq.data_ptr(), self.part_keys.data_ptr(),
+                  self.error_flag.data_ptr())
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_device", self.part_start.device)
+
     def c_struct(self) -> _Plan:
-        return _Plan(self.nseqs, self.total_tokens, self.max_new_tokens, self.window, self.max_parts,
-                     self.seq_lens.data_ptr(), None if self.cu_seqlens is None else self.cu_seqlens.data_ptr(),
-                     self.part_start.data_ptr(), self.part_seq.data_ptr(), self.part_keys.data_ptr(),
-                     self.error_flag.data_ptr())
+        return self._c
 
 
 def attention_plan(seq_lens: torch.Tensor, num_heads: int, num_kv_heads: int, cu_seqlens: Optional[torch.Tensor] = None,
@@ -907,8 +916,8 @@ def paged_attention_step(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     blocks, kv_heads, size, dim = _paged(k_cache, v_cache, device, dtype)
     if len(shape) != 3 or shape[0] != plan.total_tokens or shape[2] != dim:
         raise ValueError(f"q must be ({plan.total_tokens}, heads, {dim}), got {tuple(shape)}")
-    if plan.part_start.device != device:
-        raise ValueError(f"the plan must be on {device}, got {plan.part_start.device}")
+    if plan._device != device:
+        raise ValueError(f"the plan must be on {device}, got {plan._device}")
     heads = shape[1]
     if heads % kv_heads:
         raise ValueError(f"q's heads must be a multiple of the cache's {kv_heads}, got {heads}")

@@ -89,7 +89,7 @@ def test_long_sequences_in_many_parts_equal_float64():
     """Parts of more than one round of a workgroup's waves, joined; keys of large products."""
     i = inputs([9001, 300, 4097], [1, 1, 1], 4, 2, 128, 16, BF, seed=20, spread=4.0)
     plan = plan_of(i)
-    plan.max_parts = 3 + 8   # fewer and longer parts than would fill the GPU
+    plan = ssd.dataclasses.replace(plan, max_parts=3 + 8)   # fewer and longer parts than would fill the GPU
     ssd._enqueue("ssd_attention_plan_build", i["q"].device, ssd.ctypes.byref(plan.c_struct()))
     out, lse = call(i, plan=plan)
     starts = plan.part_start.tolist()

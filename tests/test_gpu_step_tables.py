@@ -41,11 +41,12 @@ def check(m, total=None, free_count=None, allocate=True, num_blocks=None, bits=N
     if bits is not None:
         assert want_bits == bits
     bt, fc = dev(m["table"]), dev([count])
+    flag = dev([0])
     kw = dict(free_blocks=dev(m["free"]), free_count=fc, free_count_out=fc) if allocate else {}
     t = ssd.step_tables(dev(m["computed"]), dev(m["new"]), bt, m["block"], total,
-                        rows=None if m["rows"] is None else dev(m["rows"]), num_blocks=num_blocks, **kw)
+                        rows=None if m["rows"] is None else dev(m["rows"]), num_blocks=num_blocks, error_flag=flag, **kw)
     torch.cuda.synchronize()
-    assert int(t.error_flag.item()) == want_bits
+    assert int(flag.item()) == want_bits
     got = dict(cu=t.cu_seqlens, lens=t.seq_lens, read=t.read_slot, pos=t.positions, seq=t.token_seq, slots=t.slots,
                state=t.state_slot)
     for name, g in got.items():
