@@ -11,13 +11,20 @@
 // Memory-bound: the states are the traffic (4 dk dv bytes read and written per
 // (sequence, head)). Eight lanes own a state row, in float4 pieces 8 lanes apart,
 // so that eight rows of a wave's access are whole 128-byte lines, and the two
-// sums over a row take three lane exchanges each.
+// sums over a row take three lane exchanges each. 256 sequences x 32 heads of
+// 128 x 128 take 186 us, 5.8 TB/s (a large copy reaches 5.1). A sequence's tokens
+// follow one another at 1.3 us; loading the next token's inputs ahead made that
+// 1.2 us but cost 4 to 6 % with one to four tokens.
 #include "ssd_elem.hpp"
 
 namespace ssd {
 
-constexpr int kGdnStepThreads = 128;
-constexpr int kGdnStepRows = 2;     // state rows of a lane
+constexpr int kGdnStepThreads = 64;
+// State rows of a lane: 64 or more bytes of states a lane are on their way, and beyond that more lanes do more (1 / 2 / 4
+// rows: dk 128 of 128 sequences x 32 heads x 128 rows 97 / 106 / 106 us, of 16 16.6 / 13.8 / 13.8; dk 64 of 128
+// sequences 57 / 53 / 57, of 16 10.9 / 8.1 / 8.6; dk 256 of 64 x 16 heads x 256 rows 90 / 95 with two). A wave is a
+// workgroup; two or four take 0 to 2 % longer.
+constexpr int gdn_step_rows(int dk) { return dk == 64 ? 2 : 1; }
 
 // Sum over the 8 lanes of a row; every lane gets it.
 __device__ __forceinline__ float sum8(float v) {
@@ -128,11 +135,11 @@ __global__ __launch_bounds__(kGdnStepThreads) void ssd_gdn_step_kernel(GdnStepAr
 }
 
 template <typename T, typename GT, int DK> static hipError_t launch_gdn_step_rows(GdnStepArgs a, hipStream_t stream) {
-    constexpr int ROWS = kGdnStepThreads / 8 * kGdnStepRows;
+    constexpr int R = gdn_step_rows(DK), ROWS = kGdnStepThreads / 8 * R;
     a.row_blocks = (a.dv + ROWS - 1) / ROWS;
     const int64_t blocks = (int64_t)a.S * a.H * a.row_blocks;
     if (!fits_grid(blocks, kGdnStepThreads)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((ssd_gdn_step_kernel<T, GT, DK, kGdnStepRows>), dim3((unsigned)blocks), dim3(kGdnStepThreads), 0,
+    hipLaunchKernelGGL((ssd_gdn_step_kernel<T, GT, DK, R>), dim3((unsigned)blocks), dim3(kGdnStepThreads), 0,
                        stream, a);
     return hipGetLastError();
 }
