@@ -17,7 +17,11 @@
 // once the rows of K are taken in the order key = W (q / 4) + 4 u + q mod 4 for the
 // W / 4 tiles u of a step. The cache holds values as (head dim, keys) so that the
 // left operand V^T is contiguous in memory too: keys and values go from memory to
-// the matrix cores through registers alone.
+// the matrix cores without a transposition.
+//
+// What bounds it: memory. The arithmetic of a step (32 KB of keys and values for a
+// wave of D 128) takes about a tenth of the time that its bytes do. A wave holds
+// the next step's loads in registers while it computes one, two waves a SIMD.
 #include "ssd_elem.hpp"
 
 namespace ssd {
@@ -26,9 +30,9 @@ namespace {
 
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = 64 * kAttnWaves;
-constexpr int kPartUnit = 128;     // parts are whole multiples of this many keys
-constexpr int kPartEnough = 512;   // keys of a part that are enough for its workgroup's start and end
-constexpr int kPartsPerSlot = 8;   // workgroups aimed at (4096), over those that the GPU holds at once (512)
+constexpr int kPartUnit = 256;       // parts are whole multiples of this many keys
+constexpr int kPartEnough = 1024;  // keys of a part that are enough for its workgroup's start and end
+constexpr int kPartsPerSlot = 8;   // workgroups aimed at (2048), over as many as there are CUs
 
 template <typename T> struct Mma;
 template <> struct Mma<__bf16> {
@@ -100,9 +104,9 @@ __global__ __launch_bounds__(1024) void ssd_attention_plan_kernel(AttnPlanArgs a
     int64_t total;
     scan(keys, total);
     // At most max_parts - S parts (many, so that they even out the lengths), but no shorter ones than kPartEnough keys
-    // unless there are too few to give every workgroup slot of the GPU one. One sequence of 30001 keys, 8 kv heads, in
-    // 59 / 118 / 235 parts a head: 30.9 / 33.3 / 38.1 us; 64 sequences of 276 K keys in 64 / 128 / 256 / 512 parts and as
-    // many more as there are sequences: 271 / 226 / 214 / 213 us.
+    // unless there are too few to give every CU one. One sequence of 30001 keys, 8 kv heads, in 30 / 59 parts a head:
+    // 28.0 / 32.7 us; 64 sequences of 276 K keys in 128 / 192 / 256 / 512 parts and as many more as there are sequences:
+    // 192 / 190 / 190 / 190 us.
     const int64_t target = a.max_parts - a.S, few = max(target / kPartsPerSlot, (int64_t)1);
     const int64_t most = (total + target - 1) / target, least = (total + few - 1) / few;
     const int64_t keys_of = max(most, min(least, (int64_t)kPartEnough));
@@ -138,19 +142,37 @@ __global__ __launch_bounds__(1024) void ssd_attention_plan_kernel(AttnPlanArgs a
     }
 }
 
+// How a step's keys and values pass from memory through registers and a wave's own LDS to its matrix operands. Memory is
+// read in whole lines by neighbouring lanes (a key row is contiguous, a value row's keys of a step fill a line), which
+// operands in the matrix layout are not: 16 rows, 64 bytes of each. Loads of those, straight to the operands, took 217
+// us where these take 190 (64 sequences of 276 K keys, 8 kv heads of 128, bf16: 6.0 TB/s), as long as the same loads
+// without any arithmetic: half lines do not go with the streaming policy that whole lines gain 10 % from.
+template <typename T, int D> struct AttnShape {
+    static constexpr int SZ = sizeof(T), W = 16 / SZ, U = W / 4;   // elements of 16 bytes; tiles of 16 keys of a half step
+    static constexpr int KEYS = 16 * U, SK = 2 * KEYS;             // keys of a half step and of a step (128 bytes of a value row)
+    static constexpr int CH = D / (4 * W), DB = D / 16;            // 16-byte pieces of a key row and lane; blocks of 16 of D
+    static constexpr int KPARTS = D > 128 ? 2 : 1, VPARTS = D / 64;   // stages that a step's keys, and its values, pass in
+    static constexpr int RB = D * SZ, KROWS = SK / KPARTS, DV = D / VPARTS;   // bytes of a key row; rows of a stage of keys, of values
+    static constexpr int NK = KROWS * RB / 1024, NV = DV * 128 / 1024;      // loads of a stage
+    // Rows lie 16 bytes further apart than they are long, so that the 16-byte pieces that a fragment read takes at once
+    // fall on all banks (those of keys twice on half of them), and so that all offsets from a lane's first are constants.
+    static constexpr int KPITCH = RB + 16, VPITCH = 128 + 16;
+    static constexpr int STAGE = KROWS * KPITCH > DV * VPITCH ? KROWS * KPITCH : DV * VPITCH;
+};
+
 template <typename T, int D>
-__global__ __launch_bounds__(kAttnThreads) void ssd_attention_kernel(AttnArgs a) {
-    constexpr int W = 16 / sizeof(T), U = W / 4, KEYS = 16 * U;   // elements of 16 bytes, 16-key tiles of a step, its keys
-    constexpr int CH = D / (4 * W), DB = D / 16;                  // 16-byte chunks of a key row and lane, blocks of 16 of D
-    constexpr int PAD = D + 4;
+__global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(D > 128 ? 1 : 2))) void ssd_attention_kernel(AttnArgs a) {
+    using SH = AttnShape<T, D>;
     using M = Mma<T>;
-    __shared__ float red[kAttnWaves][16][PAD];
+    constexpr int W = SH::W, U = SH::U, KEYS = SH::KEYS, SK = SH::SK, CH = SH::CH, DB = SH::DB, KPARTS = SH::KPARTS, VPARTS = SH::VPARTS, RB = SH::RB;
+    constexpr int LDS = kAttnWaves * SH::STAGE > kAttnWaves * 16 * D * 4 ? kAttnWaves * SH::STAGE : kAttnWaves * 16 * D * 4;
+    __shared__ __attribute__((aligned(16))) char lds[LDS];   // the waves' stages, then what they hand to the join
     __shared__ float wave_m[kAttnWaves][16], wave_l[kAttnWaves][16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, q = lane & 15;
     int b = blockIdx.x;
-    const int tile = b % a.tiles;
-    b /= a.tiles;
-    const int h = b % a.Hkv, p = b / a.Hkv;
+    const int h = b % a.Hkv;
+    b /= a.Hkv;
+    const int tile = b % a.tiles, p = b / a.tiles;
     const int s = a.part_seq[p];
     if (s < 0) return;
     const Span sp = span_of(a.cu_seqlens, a.seq_lens, s, a.T, a.max_new, a.window);
@@ -184,110 +206,173 @@ __global__ __launch_bounds__(kAttnThreads) void ssd_attention_kernel(AttnArgs a)
         }
     }
 
-    struct Step {
-        u32x4 k[U][CH], v[DB];
-        bool ok;   // the block of this lane's keys is in the cache
-    };
-    const int64_t head_elems = (int64_t)a.block * D;
+    // Where a step's 16-key groups lie: every lane looks up the group of its 16 bytes of a value row (piece lane mod 8),
+    // the groups of the keys are read from lanes. Keys past the end take the last group's place.
+    const int group = W * (lane & 7) / 16, last = (len - 1) & ~15;
     auto block_of = [&](int key) { return (int)(__umulhi((uint32_t)key, a.block_magic) >> a.block_shift); };
-    auto load = [&](Step &st, int key0) {
-        // keys past the end read the last ones again
-        const int vk = min(key0 + W * g, (len - 1) & ~(W - 1)), vb = block_of(vk);
-        const int kk = min(key0 + W * (q >> 2), (len - 1) & ~(W - 1)), kb = block_of(kk);
-        const int vid = table[vb], kid = table[kb];
-        st.ok = (uint32_t)vid < (uint32_t)a.num_blocks;
-        const int64_t vbase = ((int64_t)(st.ok ? vid : 0) * a.Hkv + h) * head_elems;
-        const int64_t kbase = ((int64_t)((uint32_t)kid < (uint32_t)a.num_blocks ? kid : 0) * a.Hkv + h) * head_elems;
-        const T *kp = reinterpret_cast<const T *>(a.k_cache) + kbase + W * g;
-        const T *vp = reinterpret_cast<const T *>(a.v_cache) + vbase + (vk - vb * a.block) + (int64_t)q * a.block;
+    struct Place { int key, id; };   // first key of the lane's group, its block (not yet checked)
+    auto place = [&](int key0) {
+        const int key = min(key0 + 16 * group, last);
+        return Place{key, table[block_of(key)]};
+    };
+    const int64_t head_bytes = (int64_t)a.block * RB;   // a kv head's keys, or values, of a block
+    char *stage = lds + wave * SH::STAGE;
+    char *put_key = stage + lane / (RB / 16) * SH::KPITCH + lane % (RB / 16) * 16;
+    char *put_value = stage + (lane >> 3) * SH::VPITCH + (lane & 7) * 16;
+    const char *get_key = stage + (W * (q >> 2) + (q & 3)) * SH::KPITCH + 16 * g, *get_value = stage + q * SH::VPITCH + 16 * g;
+    u32x4 kr[SH::NK], vr[SH::NV];
+    auto load_keys = [&](int key0, const Place &at, int part) {
+        const int id = (uint32_t)at.id < (uint32_t)a.num_blocks ? at.id : 0;
+        const uint64_t base = ((uint64_t)((int64_t)id * a.Hkv + h) * head_bytes) + (uint64_t)(at.key - block_of(at.key) * a.block) * RB;
+        const int lrow = lane / (RB / 16), lpiece = lane % (RB / 16) * 16;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = (int64_t)(kk - kb * a.block + 4 * u + (q & 3)) * D;
-#pragma unroll
-            for (int c = 0; c < CH; ++c) st.k[u][c] = *reinterpret_cast<const u32x4 *>(kp + row + 4 * W * c);
+        for (int j = 0; j < SH::NK; ++j) {
+            const int row0 = part * SH::KROWS + j * 1024 / RB, from = row0 / 16 * (16 / W);   // first row; a lane of its group
+            const uint64_t gb = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)base, from) |
+                                (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(base >> 32), from) << 32;
+            const int gkey = __builtin_amdgcn_readlane(at.key, from);
+            const int row = min(key0 + row0 + lrow, len - 1) - gkey;
+            kr[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(a.k_cache) + gb + (uint32_t)(row * RB + lpiece)));
         }
+    };
+    auto load_values = [&](const Place &at, int part) {
+        const int id = (uint32_t)at.id < (uint32_t)a.num_blocks ? at.id : 0;
+        const int in = at.key - block_of(at.key) * a.block + W * (lane & 7) % 16;
+        const char *from = reinterpret_cast<const char *>(a.v_cache) + ((int64_t)id * a.Hkv + h) * head_bytes +
+                           ((int64_t)(part * SH::DV + (lane >> 3)) * a.block + in) * SH::SZ;
+        const int64_t step = (int64_t)8 * a.block * SH::SZ;
 #pragma unroll
-        for (int db = 0; db < DB; ++db) st.v[db] = *reinterpret_cast<const u32x4 *>(vp + (int64_t)16 * db * a.block);
+        for (int j = 0; j < SH::NV; ++j) vr[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(from + j * step));
     };
 
     f32x4 o[DB];
 #pragma unroll
     for (int db = 0; db < DB; ++db) o[db] = f32x4{0, 0, 0, 0};
     float m = -INFINITY, l = 0.0f;   // of this lane's row; l over this lane's keys only
-    auto compute = [&](Step &st, int key0) {
-        f32x4 sc[U];
+    constexpr int STRIDE = SK * kAttnWaves;
+    int key = begin + wave * SK;
+    Place now{0, 0}, next{0, 0};
+    if (key < end) {
+        now = place(key);
+        load_keys(key, now, 0);
+        load_values(now, 0);
+        next = place(key + STRIDE);
+    }
+    for (; key < end; key += STRIDE) {
+        const bool more = key + STRIDE < end;
+        const uint64_t there = __ballot((uint32_t)now.id < (uint32_t)a.num_blocks);   // lane 16 / W i: the block of group i
+        f32x4 sc[2][U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            sc[u] = f32x4{0, 0, 0, 0};
+        for (int part = 0; part < KPARTS; ++part) {
 #pragma unroll
-            for (int c = 0; c < CH; ++c) sc[u] = M::mac(st.k[u][c], qf[c], sc[u]);
-            sc[u] *= a.scale_log2;
-        }
-        const bool masked = key0 + KEYS - 1 > all_hi || key0 + KEYS > len || key0 < all_low || __any(!st.ok);   // uniform
-        if (masked) {
-            if (!st.ok && a.error_flag != nullptr) atomicOr(a.error_flag, SSD_DATA_BAD_BLOCK);
+            for (int j = 0; j < SH::NK; ++j) {
+                *reinterpret_cast<u32x4 *>(put_key + j * 1024 / RB * SH::KPITCH) = kr[j];
+            }
+            __builtin_amdgcn_sched_barrier(0);   // (loads ahead of the stores would need registers of their own)
+            if (part + 1 < KPARTS) load_keys(key, now, part + 1);
+            else if (more) load_keys(key + STRIDE, next, 0);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int n = part; n < 2; n += KPARTS)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = key0 + W * g + 4 * u + i;
-                    if (!(st.ok && key <= hi && key >= low && key < len)) sc[u][i] = -INFINITY;
+                for (int u = 0; u < U; ++u) {
+                    const int row = (KPARTS == 1 ? KEYS * n : 0) + 4 * u;
+                    sc[n][u] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+                        sc[n][u] = M::mac(*reinterpret_cast<const u32x4 *>(get_key + row * SH::KPITCH + 64 * c), qf[c], sc[n][u]);
+                    sc[n][u] *= a.scale_log2;
+                    __builtin_amdgcn_sched_barrier(0);   // (all fragments at once do not fit the registers)
                 }
+        }
+        auto ok = [&](int n) { return (there >> ((KEYS * n + W * g) / W & ~(16 / W - 1)) & 1) != 0; };   // the block of this lane's keys
+        const bool masked = key + SK - 1 > all_hi || key + SK > len || key < all_low || ~there != 0;   // uniform
+        if (masked) {
+            if (~there != 0 && a.error_flag != nullptr && lane == 0) atomicOr(a.error_flag, SSD_DATA_BAD_BLOCK);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = key + KEYS * n + W * g + 4 * u + i;
+                        if (!(ok(n) && at <= hi && at >= low && at < len)) sc[n][u][i] = -INFINITY;
+                    }
         }
         float top = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[u][i]);
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[n][u][i]);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         if (__any(top > m)) {
-            const float now = fmaxf(m, top), f = now == -INFINITY ? 1.0f : fast_exp2(m - now);
-            m = now;
+            const float best = fmaxf(m, top), f = best == -INFINITY ? 1.0f : fast_exp2(m - best);
+            m = best;
             l *= f;
 #pragma unroll
             for (int db = 0; db < DB; ++db) o[db] *= f;
         }
         const float base = m == -INFINITY ? 0.0f : m;
+        u32x4 pf[2];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int n = 0; n < 2; ++n) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sc[u][i] = fast_exp2(sc[u][i] - base);
-                l += sc[u][i];
-            }
-        const u32x4 pf = M::operand(sc);
-        if (!masked) {
-#pragma unroll
-            for (int db = 0; db < DB; ++db) o[db] = M::mac(st.v[db], pf, o[db]);
-        } else {
-            // What a token does not see may hold anything, and 0 x infinity is no 0: its values are cleared, token by
-            // token, and only that token's rows take the sum.
-            for (int t = token0; t <= token1; ++t) {
-                const int t_hi = min(sp.len - sp.n + t, len - 1), t_low = a.window > 0 ? sp.len - sp.n + t - a.window + 1 : 0;
-                uint32_t seen[4];
+            for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int key = key0 + W * g + i * (W / 4);
-                    auto one = [&](int at) { return st.ok && at <= t_hi && at >= t_low; };
-                    seen[i] = W == 4 ? (one(key) ? 0xffffffffu : 0u)
-                                     : (one(key) ? 0x0000ffffu : 0u) | (one(key + 1) ? 0xffff0000u : 0u);
+                    sc[n][u][i] = fast_exp2(sc[n][u][i] - base);
+                    l += sc[n][u][i];
                 }
+            pf[n] = M::operand(sc[n]);
+        }
 #pragma unroll
-                for (int db = 0; db < DB; ++db) {
-                    const u32x4 v = st.v[db];
-                    const f32x4 with = M::mac(u32x4{v[0] & seen[0], v[1] & seen[1], v[2] & seen[2], v[3] & seen[3]}, pf, o[db]);
-                    if (token == t) o[db] = with;
+        for (int part = 0; part < VPARTS; ++part) {
+#pragma unroll
+            for (int j = 0; j < SH::NV; ++j) *reinterpret_cast<u32x4 *>(put_value + 8 * j * SH::VPITCH) = vr[j];
+            __builtin_amdgcn_sched_barrier(0);
+            if (part + 1 < VPARTS) load_values(now, part + 1);
+            else if (more) load_values(next, 0);
+            uint32_t from = lds_addr(get_value);
+            auto value = [&](int db, int n) { return *(const __attribute__((address_space(3))) u32x4 *)(uintptr_t)(from + 16 * db * SH::VPITCH + 64 * n); };
+            if (!masked) {
+#pragma unroll
+                for (int db = 0; db < DB / VPARTS; ++db)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        o[part * DB / VPARTS + db] = M::mac(value(db, n), pf[n], o[part * DB / VPARTS + db]);
+                        if (n == 1 && db % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+                    }
+            } else {
+                // What a token does not see may hold anything, and 0 x infinity is no 0: its values are cleared, token by
+                // token, and only that token's rows take the sum.
+                for (int t = token0; t <= token1; ++t) {
+                    asm("" : "+v"(from));   // (the values are read again for every token: all of them do not fit the registers)
+                    const int t_hi = min(sp.len - sp.n + t, len - 1), t_low = a.window > 0 ? sp.len - sp.n + t - a.window + 1 : 0;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        uint32_t seen[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int at = key + KEYS * n + W * g + i * (W / 4);
+                            auto one = [&](int k) { return ok(n) && k <= t_hi && k >= t_low; };
+                            seen[i] = W == 4 ? (one(at) ? 0xffffffffu : 0u)
+                                             : (one(at) ? 0x0000ffffu : 0u) | (one(at + 1) ? 0xffff0000u : 0u);
+                        }
+#pragma unroll
+                        for (int db = 0; db < DB / VPARTS; ++db) {
+                            const u32x4 v = value(db, n);
+                            f32x4 &to = o[part * DB / VPARTS + db];
+                            const f32x4 with = M::mac(u32x4{v[0] & seen[0], v[1] & seen[1], v[2] & seen[2], v[3] & seen[3]}, pf[n], to);
+                            if (token == t) to = with;
+                        }
+                    }
                 }
             }
         }
-    };
-
-    constexpr int STRIDE = KEYS * kAttnWaves;
-    for (int key = begin + wave * KEYS; key < end; key += STRIDE) {
-        Step st;
-        load(st, key);
-        compute(st, key);
+        now = next;
+        if (more) next = place(key + 2 * STRIDE);
     }
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
@@ -301,8 +386,10 @@ __global__ __launch_bounds__(kAttnThreads) void ssd_attention_kernel(AttnArgs a)
     float top = -INFINITY;
     for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, wave_m[w][q]);
     const float f = top == -INFINITY ? 0.0f : fast_exp2(m - top);
+    float *red = reinterpret_cast<float *>(lds);   // (wave, row, D), four values of a row at a time in the row's own order
+    auto red_at = [&](int w, int row, int d4) { return ((w * 16 + row) * (D / 4) + (d4 ^ (row & 15))) * 4; };
 #pragma unroll
-    for (int db = 0; db < DB; ++db) *reinterpret_cast<f32x4 *>(&red[wave][q][16 * db + 4 * g]) = o[db] * f;
+    for (int db = 0; db < DB; ++db) *reinterpret_cast<f32x4 *>(red + red_at(wave, q, 4 * db + g)) = o[db] * f;
     __syncthreads();
     for (int i = threadIdx.x; i < 16 * D / 4; i += kAttnThreads) {
         const int row = i / (D / 4), d = i % (D / 4) * 4, rr = tile * 16 + row;
@@ -312,7 +399,7 @@ __global__ __launch_bounds__(kAttnThreads) void ssd_attention_kernel(AttnArgs a)
         f32x4 v{0, 0, 0, 0};
         for (int w = 0; w < kAttnWaves; ++w) {
             sum += best == -INFINITY ? 0.0f : wave_l[w][row] * fast_exp2(wave_m[w][row] - best);
-            v += *reinterpret_cast<const f32x4 *>(&red[w][row][d]);
+            v += *reinterpret_cast<const f32x4 *>(red + red_at(w, row, d / 4));
         }
         if (nparts == 1) {
             const int64_t t = sp.t0 + rr / a.group;

@@ -236,8 +236,8 @@ struct AttnArgs {
     int32_t table_rows, max_blocks, num_blocks, block;
     uint32_t block_magic, block_shift;  // key / block = mulhi(key, block_magic) >> block_shift, for 31-bit keys
 };
-// Workgroups that an attention call aims at: 16 for each of the 256 CUs.
-constexpr int32_t kAttnWorkgroups = 4096;
+// Workgroups that an attention call aims at: 8 for each of the 256 CUs.
+constexpr int32_t kAttnWorkgroups = 2048;
 hipError_t launch_attention(const AttnArgs &a, bool bf16, int D, hipStream_t stream);
 
 // Block tables and slot maps of one step (see ssd_tables.hip).

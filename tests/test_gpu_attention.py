@@ -104,7 +104,7 @@ def test_plan_covers_every_key_once():
         lens, cu = torch.tensor(lengths, dtype=torch.int32).cuda(), torch.tensor([0] + counts).cumsum(0).to(torch.int32).cuda()
         plan = ssd.attention_plan(lens, 8, 2, cu_seqlens=cu, total_tokens=sum(counts), max_new_tokens=4, window=window)
         part, starts, seqs = int(plan.part_keys.item()), plan.part_start.tolist(), plan.part_seq.tolist()
-        assert part > 0 and part % 128 == 0 and starts[0] == 0 and starts[-1] <= plan.max_parts
+        assert part > 0 and part % 256 == 0 and starts[0] == 0 and starts[-1] <= plan.max_parts
         want = []
         for s, (n, new) in enumerate(zip(lengths, counts)):
             low = max(0, n - new - window + 1) // 32 * 32 if window else 0
