@@ -160,7 +160,8 @@ template <typename T, int D> struct AttnShape {
     static constexpr int STAGE = KROWS * KPITCH > DV * VPITCH ? KROWS * KPITCH : DV * VPITCH;
 };
 
-template <typename T, int D>
+// STREAM: nobody else reads the keys and values that a workgroup does (one tile of rows).
+template <typename T, int D, bool STREAM>
 __global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(D > 128 ? 1 : 2))) void ssd_attention_kernel(AttnArgs a) {
     using SH = AttnShape<T, D>;
     using M = Mma<T>;
@@ -169,10 +170,12 @@ __global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(D 
     __shared__ __attribute__((aligned(16))) char lds[LDS];   // the waves' stages, then what they hand to the join
     __shared__ float wave_m[kAttnWaves][16], wave_l[kAttnWaves][16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, q = lane & 15;
-    int b = blockIdx.x;
-    const int h = b % a.Hkv;
-    b /= a.Hkv;
-    const int tile = b % a.tiles, p = b / a.tiles;
+    // Workgroups go to the 8 XCDs in turn: the tiles of one part and head to the same one, one after the other, so that all
+    // but the first find its lines in that L2 (64 sequences of 2000 to 4331 keys, 4 tokens, 4 kv heads with 8 query heads
+    // each: 119 us, 168 with the tiles on any XCD; two tiles to a workgroup leave one wave a SIMD, 123 us).
+    const int in = blockIdx.x % (8 * a.tiles), x = blockIdx.x / (8 * a.tiles) * 8 + in % 8;
+    const int tile = in / 8, h = x % a.Hkv, p = x / a.Hkv;
+    if (p >= a.max_parts) return;
     const int s = a.part_seq[p];
     if (s < 0) return;
     const Span sp = span_of(a.cu_seqlens, a.seq_lens, s, a.T, a.max_new, a.window);
@@ -221,6 +224,10 @@ __global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(D 
     char *put_value = stage + (lane >> 3) * SH::VPITCH + (lane & 7) * 16;
     const char *get_key = stage + (W * (q >> 2) + (q & 3)) * SH::KPITCH + 16 * g, *get_value = stage + q * SH::VPITCH + 16 * g;
     u32x4 kr[SH::NK], vr[SH::NV];
+    auto stream = [](const u32x4 *at) {
+        if constexpr (STREAM) return __builtin_nontemporal_load(at);
+        else return *at;
+    };
     auto load_keys = [&](int key0, const Place &at, int part) {
         const int id = (uint32_t)at.id < (uint32_t)a.num_blocks ? at.id : 0;
         const uint64_t base = ((uint64_t)((int64_t)id * a.Hkv + h) * head_bytes) + (uint64_t)(at.key - block_of(at.key) * a.block) * RB;
@@ -232,7 +239,7 @@ __global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(D 
                                 (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(base >> 32), from) << 32;
             const int gkey = __builtin_amdgcn_readlane(at.key, from);
             const int row = min(key0 + row0 + lrow, len - 1) - gkey;
-            kr[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(a.k_cache) + gb + (uint32_t)(row * RB + lpiece)));
+            kr[j] = stream(reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(a.k_cache) + gb + (uint32_t)(row * RB + lpiece)));
         }
     };
     auto load_values = [&](const Place &at, int part) {
@@ -242,7 +249,7 @@ __global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(D 
                            ((int64_t)(part * SH::DV + (lane >> 3)) * a.block + in) * SH::SZ;
         const int64_t step = (int64_t)8 * a.block * SH::SZ;
 #pragma unroll
-        for (int j = 0; j < SH::NV; ++j) vr[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(from + j * step));
+        for (int j = 0; j < SH::NV; ++j) vr[j] = stream(reinterpret_cast<const u32x4 *>(from + j * step));
     };
 
     f32x4 o[DB];
@@ -566,9 +573,11 @@ __global__ __launch_bounds__(256) void ssd_kv_write_tile_kernel(KvWriteArgs a) {
 }
 
 template <typename T, int D> hipError_t launch_attention_d(const AttnArgs &a, hipStream_t stream) {
-    const int64_t blocks = (int64_t)a.max_parts * a.Hkv * a.tiles, joins = (int64_t)a.T * a.Hq;
+    const int64_t blocks = ((int64_t)a.max_parts * a.Hkv + 7) / 8 * 8 * a.tiles, joins = (int64_t)a.T * a.Hq;
     if (!fits_grid(blocks, kAttnThreads) || !fits_grid(joins, 256)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((ssd_attention_kernel<T, D>), dim3((unsigned)blocks), dim3(kAttnThreads), 0, stream, a);
+    const dim3 grid((unsigned)blocks), block(kAttnThreads);
+    if (a.tiles == 1) hipLaunchKernelGGL((ssd_attention_kernel<T, D, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((ssd_attention_kernel<T, D, false>), grid, block, 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((ssd_attention_join_kernel<T, D>), dim3((unsigned)joins), dim3(256), 0, stream, a);
