@@ -512,7 +512,8 @@ __global__ __launch_bounds__(256) void ssd_kv_write_kernel(KvWriteArgs a) {
 
 // The same for many tokens: 64 tokens of one head a workgroup, the values turned in LDS, so that a store's lanes are
 // tokens, whose places in a prompt's block follow each other: a store writes whole lines of the values (single values
-// scattered took 7 times as long).
+// scattered took 6 times as long). 35576 tokens x 8 heads x 128 bf16 take 55 us, 5.3 TB/s, a large copy's rate; 69 without
+// the streaming policy on what is read and on the keys, 80 with it on the values too, whose lines two stores fill.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void ssd_kv_write_tile_kernel(KvWriteArgs a) {
     constexpr int W = 16 / sizeof(T), PER = D / W, ROW = D * sizeof(T) + 8;   // 16-byte pieces of a row; its bytes in LDS
@@ -529,22 +530,23 @@ __global__ __launch_bounds__(256) void ssd_kv_write_tile_kernel(KvWriteArgs a) {
         }
         slots[threadIdx.x] = slot;
     }
-    Raw16<T> k[ROUNDS], v[ROUNDS];
+    typedef u32x4 Vec __attribute__((aligned(2)));   // (rows start on any element)
+    u32x4 k[ROUNDS], v[ROUNDS];
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) {
         const int i = r * 256 + threadIdx.x;
         const int64_t t = t0 + i / PER, e = (int64_t)h * D + i % PER * W;
         if (t < a.T) {
-            k[r] = *reinterpret_cast<const Raw16<T> *>(reinterpret_cast<const T *>(a.k) + t * a.k_stride + e);
-            v[r] = *reinterpret_cast<const Raw16<T> *>(reinterpret_cast<const T *>(a.v) + t * a.v_stride + e);
+            k[r] = __builtin_nontemporal_load(reinterpret_cast<const Vec *>(reinterpret_cast<const T *>(a.k) + t * a.k_stride + e));
+            v[r] = __builtin_nontemporal_load(reinterpret_cast<const Vec *>(reinterpret_cast<const T *>(a.v) + t * a.v_stride + e));
         }
     }
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) {
         const int i = r * 256 + threadIdx.x;
         u32x2 *to = reinterpret_cast<u32x2 *>(tile + i / PER * ROW + i % PER * 16);
-        to[0] = u32x2{v[r].w[0], v[r].w[1]};
-        to[1] = u32x2{v[r].w[2], v[r].w[3]};
+        to[0] = u32x2{v[r][0], v[r][1]};
+        to[1] = u32x2{v[r][2], v[r][3]};
     }
     __syncthreads();
 #pragma unroll
@@ -553,7 +555,7 @@ __global__ __launch_bounds__(256) void ssd_kv_write_tile_kernel(KvWriteArgs a) {
         if (slot < 0) continue;
         const int block = slot / a.block, at = slot - block * a.block;
         T *to = reinterpret_cast<T *>(a.k_cache) + (((int64_t)block * a.Hkv + h) * a.block + at) * D + i % PER * W;
-        *reinterpret_cast<u32x4 *>(to) = u32x4{k[r].w[0], k[r].w[1], k[r].w[2], k[r].w[3]};
+        __builtin_nontemporal_store(k[r], reinterpret_cast<u32x4 *>(to));
     }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, slot = slots[lane];
     if (slot < 0) return;
@@ -604,11 +606,13 @@ hipError_t launch_attention(const AttnArgs &a, bool bf16, int D, hipStream_t str
     return bf16 ? launch_attention_t<__bf16>(a, D, stream) : launch_attention_t<float>(a, D, stream);
 }
 
-// From this many tokens on the values are turned in LDS.
-constexpr int kTileTokens = 1024;
+// From this many rows of heads on the values are turned in LDS (a prompt of 512 / 1024 tokens x 8 heads 5.6 / 6.5 us, 6.2 /
+// 10.2 without; 2048 / 4096 x 2 heads 5.5 / 6.1, 4.5 / 6.6 without; 512 / 1024 single tokens x 8 heads 14.0 / 16.3, 7.9 /
+// 23.2 without).
+constexpr int64_t kTileRows = 8192;
 
 template <typename T> static hipError_t launch_kv_write_t(const KvWriteArgs &a, hipStream_t stream) {
-    const bool tiles = a.T >= kTileTokens;
+    const bool tiles = (int64_t)a.T * a.Hkv >= kTileRows;
     const int64_t lanes = (int64_t)a.T * a.Hkv * a.D * sizeof(T) / 16;
     const int64_t blocks = tiles ? ((int64_t)a.T + 63) / 64 * a.Hkv : (lanes + 255) / 256;
     if (!fits_grid(blocks, 256)) return hipErrorInvalidConfiguration;

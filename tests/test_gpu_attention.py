@@ -272,7 +272,8 @@ def check_write(i, flag=0):
 @pytest.mark.parametrize("T,Hkv,D,block,dtype,pad,run", [
     (1, 1, 64, 16, F32, 0, False), (1, 8, 128, 16, BF, 0, False), (7, 3, 64, 48, BF, 1, False), (64, 2, 256, 16, BF, 8, True),
     (130, 2, 128, 64, F32, 3, True), (257, 1, 64, 16, BF, 0, True), (300, 4, 128, 528, BF, 2, True), (65, 8, 64, 32, F32, 0, False),
-    (1000, 2, 128, 256, BF, 0, True), (33, 1, 256, 16, F32, 1, True),
+    (1000, 2, 128, 256, BF, 0, True), (33, 1, 256, 16, F32, 1, True), (1025, 8, 128, 16, BF, 0, True), (2731, 3, 64, 48, BF, 1, True),
+    (8195, 1, 256, 16, F32, 3, False), (4100, 2, 64, 528, F32, 0, True), (2050, 4, 256, 32, BF, 5, False), (8200, 1, 128, 64, F32, 1, True),
 ])
 def test_cache_write(T, Hkv, D, block, dtype, pad, run):
     log(f"cache write {T, Hkv, D, block, dtype, pad, run}")
@@ -281,8 +282,8 @@ def test_cache_write(T, Hkv, D, block, dtype, pad, run):
 
 
 def test_cache_write_skips_and_refuses():
-    for run in (False, True):
-        i = write_inputs(90, 2, 64, 16, BF, seed=5, run=run)
+    for T, run in ((90, False), (90, True), (4200, False), (4200, True)):   # (both kernels)
+        i = write_inputs(T, 2, 64, 16, BF, seed=5, run=run)
         i["slots"][::7] = -1
         i["slots"][3] = i["kc"].shape[0] * 16
         i["slots"][50] = 2 ** 31 - 1
