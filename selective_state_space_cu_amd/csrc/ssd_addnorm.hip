@@ -7,7 +7,8 @@
 //
 // Memory-bound: x, the residual and the outputs pass once; a row stays in the
 // registers of its team of lanes (lane l holds vectors l, l + TEAM, ..) between
-// the loads, the sum of squares, the maxima and the stores.
+// the loads, the sum of squares, the maxima and the stores. 35576 x 4096 bf16 to
+// e4m3 in groups of 128 takes 168 us, 6.1 TB/s (a large copy reaches 5.1).
 #include <algorithm>
 
 #include "ssd_norm.hpp"
@@ -43,6 +44,16 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v, int lanes) {
     return v;
 }
 
+// Loads and stores of 16 bytes with the streaming policy (narrower ones share their lines and go without).
+template <typename Raw> __device__ __forceinline__ Raw load_streamed(const void *p) {
+    if constexpr (sizeof(Raw) == 16) return __builtin_bit_cast(Raw, __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p)));
+    else return *reinterpret_cast<const Raw *>(p);
+}
+template <typename Raw> __device__ __forceinline__ void store_streamed(void *p, const Raw &v) {
+    if constexpr (sizeof(Raw) == 16) __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4 *>(p));
+    else *reinterpret_cast<Raw *>(p) = v;
+}
+
 // Where a row's scales come from: none (no 8 bits), a given one, the whole row, groups inside a wave's lanes, larger groups.
 enum Scales { kNoScale, kGiven, kRowScale, kLaneGroups, kWideGroups };
 
@@ -69,12 +80,16 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void ssd_add_rms_norm_kern
     auto live = [&](int r) { return r * SPAN + lane * V < C; };
     Raw rx[R], rr[R];
     Weights w[R];
+    auto load = [&](auto from) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (live(r)) {
-            rx[r] = *reinterpret_cast<const Raw *>(x + r * SPAN);
-            if (a.residual) rr[r] = *reinterpret_cast<const Raw *>(res + r * SPAN);
-        }
+        for (int r = 0; r < R; ++r)
+            if (live(r)) {
+                rx[r] = from(x + r * SPAN);
+                if (a.residual) rr[r] = from(res + r * SPAN);
+            }
+    };
+    if (a.stream) load([](const T *at) { return load_streamed<Raw>(at); });
+    else load([](const T *at) { return *reinterpret_cast<const Raw *>(at); });
 #pragma unroll
     for (int r = 0; r < R; ++r)
         if (live(r)) {
@@ -100,7 +115,10 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void ssd_add_rms_norm_kern
 #pragma unroll
             for (int i = 0; i < V; ++i) v[r * V + i] += y[i];
         }
-        if (a.residual_out) *reinterpret_cast<Raw *>(res_out + r * SPAN) = IO::pack(v + r * V);
+        if (a.residual_out) {
+            if (a.stream) store_streamed(res_out + r * SPAN, IO::pack(v + r * V));
+            else *reinterpret_cast<Raw *>(res_out + r * SPAN) = IO::pack(v + r * V);
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i) sq = fmaf(v[r * V + i], v[r * V + i], sq);
     }
@@ -226,7 +244,13 @@ template <typename T> static hipError_t launch_addnorm_t(const AddNormArgs &a, b
     return launch_addnorm_v<T, 1>(a, e4m3, stream);
 }
 
-hipError_t launch_add_rms_norm(const AddNormArgs &a, bool bf16, bool e4m3, hipStream_t stream) {
+// Inputs and the residual that the last-level cache (256 MB) cannot hold are streamed past it (35576 x 4096 bf16 to e4m3 in
+// groups of 128 184 -> 168 us, to bf16 203 -> 195, 16000 x 8192 float32 378 -> 377; 4096 x 4096 bf16, which it holds, would
+// go from 24.8 to 25.6).
+constexpr int64_t kStreamBytes = int64_t(256) << 20;
+
+hipError_t launch_add_rms_norm(AddNormArgs a, bool bf16, bool e4m3, hipStream_t stream) {
+    a.stream = (int64_t)a.rows * a.channels * (bf16 ? 2 : 4) * (1 + (a.residual != nullptr) + (a.residual_out != nullptr)) > kStreamBytes;
     return bf16 ? launch_addnorm_t<__bf16>(a, e4m3, stream) : launch_addnorm_t<float>(a, e4m3, stream);
 }
 

@@ -262,8 +262,9 @@ struct AddNormArgs {
     int64_t x_stride, residual_stride, residual_out_stride, out_stride;
     int32_t rows, channels, group;      // group: channels that share a scale
     float eps;
+    int32_t stream;                     // inputs and residual_out pass the caches by (set by the launch)
 };
-hipError_t launch_add_rms_norm(const AddNormArgs &a, bool bf16, bool e4m3, hipStream_t stream);
+hipError_t launch_add_rms_norm(AddNormArgs a, bool bf16, bool e4m3, hipStream_t stream);
 
 struct MetaArgs {
     const int32_t *cu_seqlens;
