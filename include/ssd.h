@@ -539,8 +539,9 @@ ssd_status ssd_group_norm(
  *  error_flag      int32 [1] or NULL: a slot >= num_slots sets
  *                  SSD_DATA_BAD_SLOT, a sequence outside [0, total_tokens]
  *                  SSD_DATA_BAD_CU_SEQLENS; that sequence is skipped entirely.
- * Supported: dk in {64, 128, 256}, any dv >= 1, nheads % nkheads == 0. o must
- * not overlap an input.
+ * Rows behind the last sequence's tokens (a padded batch) are left as they were.
+ * Supported: dk in {64, 128, 256}, any dv >= 1, nheads % nkheads == 0, up to
+ * 2^30 tokens. o must not overlap an input.
  * Precision: all arithmetic and the state in float32; o is rounded once (to
  * nearest even). Results do not depend on the batch around a sequence.
  * Errors: SSD_ERR_DTYPE, SSD_ERR_SHAPE (sizes, strides, alignment of the cache
@@ -665,8 +666,10 @@ typedef struct {
 
 /*
  * Builds the plan. A sequence whose tokens are outside [0, total_tokens] or
- * more than max_new_tokens sets SSD_DATA_BAD_CU_SEQLENS and is left out: the
- * attention writes nothing for it. Negative seq_lens count as 0.
+ * more than max_new_tokens, or that has more than 2^30 keys, sets
+ * SSD_DATA_BAD_CU_SEQLENS and is left out: the attention writes nothing for it.
+ * Negative seq_lens count as 0. seq_lens and cu_seqlens stay as they are until
+ * the calls that use the plan have run.
  * Errors: SSD_ERR_NULL_ARG, SSD_ERR_SHAPE (sizes), SSD_ERR_CAPACITY
  * (max_parts <= nseqs), SSD_ERR_HIP.
  */
@@ -683,7 +686,8 @@ ssd_status ssd_attention_plan_build(const ssd_attention_plan *plan, void *stream
  *     lse[t,h] = log sum_i e_i.
  * Tokens that see no key (an empty sequence, or p < 0), or only such whose
  * products are all -infinity, get 0 and lse -infinity. What the cache holds
- * where a token does not see it has no effect, whatever it is.
+ * where a token does not see it has no effect, whatever it is. Rows of q behind
+ * the last sequence's (a padded batch) leave theirs of out and lse as they were.
  *  q, out          element type `dtype`, (total_tokens, nheads, head_dim), rows
  *                  *_stride elements apart (at least the row, at most 2^26)
  *  k_cache, v_cache  as in ssd_kv_cache_write, 16-byte aligned

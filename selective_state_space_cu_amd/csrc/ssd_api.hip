@@ -494,8 +494,8 @@ ssd_status ssd_gated_delta_step(const void *q, int64_t q_stride, const void *k, 
                                 const int32_t *write_slot, void *o, int64_t o_stride, int32_t *error_flag,
                                 void *stream) {
     if (!known_dtype(in_dtype) || !known_dtype(gate_dtype)) return SSD_ERR_DTYPE;
-    if (nseqs < 0 || total_tokens < 0 || num_slots < 0 || nheads <= 0 || nkheads <= 0 || dk <= 0 || dv <= 0 ||
-        nheads % nkheads != 0 || qk_eps != qk_eps || scale != scale)
+    if (nseqs < 0 || total_tokens < 0 || total_tokens > (1 << 30) || num_slots < 0 || nheads <= 0 || nkheads <= 0 ||
+        dk <= 0 || dv <= 0 || nheads % nkheads != 0 || qk_eps != qk_eps || scale != scale)
         return SSD_ERR_SHAPE;
     if (cu_seqlens == nullptr && total_tokens != nseqs) return SSD_ERR_SHAPE;
     if (!(dk == 64 || dk == 128 || dk == 256)) return SSD_ERR_UNSUPPORTED;

@@ -22,6 +22,8 @@
 // What bounds it: memory. The arithmetic of a step (32 KB of keys and values for a
 // wave of D 128) takes about a tenth of the time that its bytes do. A wave holds
 // the next step's loads in registers while it computes one, two waves a SIMD.
+#include <algorithm>
+
 #include "ssd_elem.hpp"
 
 namespace ssd {
@@ -58,6 +60,8 @@ template <> struct Mma<float> {
 
 template <typename T> struct __attribute__((packed, aligned(sizeof(T)))) Raw16 { uint32_t w[4]; };
 
+constexpr int kMostKeys = 1 << 30;   // of a sequence: positions stay in 32 bits past a step's end
+
 // Tokens and keys of one sequence, as the plan and the kernels see them.
 struct Span {
     int t0, n, len, lo;   // first token, tokens, keys, first key that any token sees (a multiple of 32)
@@ -68,7 +72,7 @@ __device__ __forceinline__ Span span_of(const int32_t *cu, const int32_t *lens, 
     Span r;
     r.t0 = cu != nullptr ? cu[s] : s;
     const int t1 = cu != nullptr ? cu[s + 1] : s + 1;
-    r.bad = r.t0 < 0 || t1 < r.t0 || t1 > T || t1 - r.t0 > max_new;
+    r.bad = r.t0 < 0 || t1 < r.t0 || t1 > T || t1 - r.t0 > max_new || lens[s] > kMostKeys;
     r.n = r.bad ? 0 : t1 - r.t0;
     r.len = max(lens[s], 0);
     const int64_t lo = window > 0 ? (int64_t)r.len - r.n - window + 1 : 0;
@@ -110,7 +114,7 @@ __global__ __launch_bounds__(1024) void ssd_attention_plan_kernel(AttnPlanArgs a
     const int64_t target = a.max_parts - a.S, few = max(target / kPartsPerSlot, (int64_t)1);
     const int64_t most = (total + target - 1) / target, least = (total + few - 1) / few;
     const int64_t keys_of = max(most, min(least, (int64_t)kPartEnough));
-    const int part = (int)max((keys_of + kPartUnit - 1) / kPartUnit * kPartUnit, (int64_t)kPartUnit);
+    const int part = (int)min(max((keys_of + kPartUnit - 1) / kPartUnit * kPartUnit, (int64_t)kPartUnit), (int64_t)kMostKeys);
     int64_t carry = 0;
     for (int base = 0; base < a.S; base += 1024) {
         const int s = base + tid;
@@ -427,12 +431,12 @@ __global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(D 
     }
 }
 
-// Joins the parts of sequences that have several: one workgroup per token and head.
+// Joins the parts of sequences that have several: blocks_per_token workgroups a token take its heads in turn.
 template <typename T, int D>
-__global__ __launch_bounds__(256) void ssd_attention_join_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256) void ssd_attention_join_kernel(AttnArgs a, int blocks_per_token) {
     constexpr int LANES = D / 4, GROUPS = 256 / LANES;
     __shared__ float red[GROUPS][D], red_m[4], red_l[GROUPS];
-    const int t = blockIdx.x / a.Hq, head = blockIdx.x % a.Hq;
+    const int t = blockIdx.x / blocks_per_token;
     int s = t;
     if (a.cu_seqlens != nullptr) {
         int lo = 0, hi = a.S;
@@ -446,42 +450,46 @@ __global__ __launch_bounds__(256) void ssd_attention_join_kernel(AttnArgs a) {
     if (t < sp.t0 || t >= sp.t0 + sp.n) return;
     const int first = a.part_start[s], nparts = a.part_start[s + 1] - first;
     if (nparts <= 1) return;
-    const int rows = a.max_new * a.group, r = (t - sp.t0) * a.group + head % a.group, h = head / a.group;
-    // the largest maximum, then the sums: independent loads, so that all of a lane's are on their way at once
-    const int64_t at0 = ((int64_t)first * a.Hkv + h) * rows + r, step = (int64_t)a.Hkv * rows;
-    float best = -INFINITY;
-    for (int k = threadIdx.x; k < nparts; k += 256) best = fmaxf(best, a.part_ml[2 * (at0 + k * step)]);
+    const int rows = a.max_new * a.group;
+    for (int head = blockIdx.x % blocks_per_token; head < a.Hq; head += blocks_per_token) {
+        const int r = (t - sp.t0) * a.group + head % a.group, h = head / a.group;
+        // the largest maximum, then the sums: independent loads, so that all of a lane's are on their way at once
+        const int64_t at0 = ((int64_t)first * a.Hkv + h) * rows + r, step = (int64_t)a.Hkv * rows;
+        float best = -INFINITY;
+        for (int k = threadIdx.x; k < nparts; k += 256) best = fmaxf(best, a.part_ml[2 * (at0 + k * step)]);
 #pragma unroll
-    for (int x = 32; x >= 1; x >>= 1) best = fmaxf(best, __shfl_xor(best, x));
-    if ((threadIdx.x & 63) == 0) red_m[threadIdx.x >> 6] = best;
-    __syncthreads();
-    best = fmaxf(fmaxf(red_m[0], red_m[1]), fmaxf(red_m[2], red_m[3]));
-    const float base = best == -INFINITY ? 0.0f : best;
-    const int grp = threadIdx.x / LANES, d = threadIdx.x % LANES * 4;
-    float l = 0.0f;
-    f32x4 v{0, 0, 0, 0};
+        for (int x = 32; x >= 1; x >>= 1) best = fmaxf(best, __shfl_xor(best, x));
+        __syncthreads();   // the head before has been read
+        if ((threadIdx.x & 63) == 0) red_m[threadIdx.x >> 6] = best;
+        __syncthreads();
+        best = fmaxf(fmaxf(red_m[0], red_m[1]), fmaxf(red_m[2], red_m[3]));
+        const float base = best == -INFINITY ? 0.0f : best;
+        const int grp = threadIdx.x / LANES, d = threadIdx.x % LANES * 4;
+        float l = 0.0f;
+        f32x4 v{0, 0, 0, 0};
 #pragma unroll 4
-    for (int k = grp; k < nparts; k += GROUPS) {
-        const int64_t at = at0 + k * step;
-        const float e = fast_exp2(a.part_ml[2 * at] - base);
-        l += a.part_ml[2 * at + 1] * e;
-        v += *reinterpret_cast<const f32x4 *>(a.part_o + at * D + d) * e;
-    }
-    *reinterpret_cast<f32x4 *>(&red[grp][d]) = v;
-    if (d == 0) red_l[grp] = l;
-    __syncthreads();
-    if (grp != 0) return;
-    l = 0.0f;
-    v = f32x4{0, 0, 0, 0};
-    for (int k = 0; k < GROUPS; ++k) {
-        l += red_l[k];
-        v += *reinterpret_cast<const f32x4 *>(&red[k][d]);
-    }
-    T *out = reinterpret_cast<T *>(a.out) + t * a.out_stride + (int64_t)head * D + d;
-    const float inv = best == -INFINITY ? 0.0f : 1.0f / l;
+        for (int k = grp; k < nparts; k += GROUPS) {
+            const int64_t at = at0 + k * step;
+            const float e = fast_exp2(a.part_ml[2 * at] - base);
+            l += a.part_ml[2 * at + 1] * e;
+            v += *reinterpret_cast<const f32x4 *>(a.part_o + at * D + d) * e;
+        }
+        *reinterpret_cast<f32x4 *>(&red[grp][d]) = v;
+        if (d == 0) red_l[grp] = l;
+        __syncthreads();
+        if (grp != 0) continue;
+        l = 0.0f;
+        v = f32x4{0, 0, 0, 0};
+        for (int k = 0; k < GROUPS; ++k) {
+            l += red_l[k];
+            v += *reinterpret_cast<const f32x4 *>(&red[k][d]);
+        }
+        T *out = reinterpret_cast<T *>(a.out) + t * a.out_stride + (int64_t)head * D + d;
+        const float inv = best == -INFINITY ? 0.0f : 1.0f / l;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) out[k] = (T)(v[k] * inv);
-    if (a.lse != nullptr && d == 0) a.lse[(int64_t)t * a.Hq + head] = (best + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+        for (int k = 0; k < 4; ++k) out[k] = (T)(v[k] * inv);
+        if (a.lse != nullptr && d == 0) a.lse[(int64_t)t * a.Hq + head] = (best + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+    }
 }
 
 // Copies the rows of new tokens to their slots: keys as they are, values turned. One token and 16 bytes of its row a lane:
@@ -574,15 +582,19 @@ __global__ __launch_bounds__(256) void ssd_kv_write_tile_kernel(KvWriteArgs a) {
     }
 }
 
+constexpr int kJoinWorkgroups = 2048;
+
 template <typename T, int D> hipError_t launch_attention_d(const AttnArgs &a, hipStream_t stream) {
-    const int64_t blocks = ((int64_t)a.max_parts * a.Hkv + 7) / 8 * 8 * a.tiles, joins = (int64_t)a.T * a.Hq;
+    // (many tokens have few parts each, or none: no more workgroups than see to that at once)
+    const int per_token = std::max(1, std::min(a.Hq, (kJoinWorkgroups + a.T - 1) / a.T));
+    const int64_t blocks = ((int64_t)a.max_parts * a.Hkv + 7) / 8 * 8 * a.tiles, joins = (int64_t)a.T * per_token;
     if (!fits_grid(blocks, kAttnThreads) || !fits_grid(joins, 256)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)blocks), block(kAttnThreads);
     if (a.tiles == 1) hipLaunchKernelGGL((ssd_attention_kernel<T, D, true>), grid, block, 0, stream, a);
     else hipLaunchKernelGGL((ssd_attention_kernel<T, D, false>), grid, block, 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((ssd_attention_join_kernel<T, D>), dim3((unsigned)joins), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((ssd_attention_join_kernel<T, D>), dim3((unsigned)joins), dim3(256), 0, stream, a, per_token);
     return hipGetLastError();
 }
 

@@ -197,6 +197,63 @@ def test_sequences_outside_the_batch_or_too_long_are_left_out():
         assert (out[left] == 3).all() and torch.equal(out[:2], good[:2])
 
 
+def test_lengths_past_the_limit_and_below_zero():
+    """A sequence of more than 2^30 keys is left out; a negative length counts as none."""
+    i = inputs([40, 50, 20], [1] * 3, 4, 2, 64, 16, BF, seed=29)
+    good, _ = call(i)
+    i["lens"][1] = 2 ** 30 + 1
+    plan = plan_of(i)
+    assert int(plan.error_flag.item()) == ssd.DATA_BAD_CU_SEQLENS
+    out = torch.full_like(good, 3.0)
+    ssd.paged_attention_step(i["q"], i["kc"], i["vc"], i["table"], plan, out=out)
+    torch.cuda.synchronize()
+    assert (out[1] == 3).all() and torch.equal(out[[0, 2]], good[[0, 2]])
+    i["lens"][1] = 2 ** 30   # more than the table holds: what it holds counts
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ssd.paged_attention_step(i["q"], i["kc"], i["vc"], i["table"], plan_of(i), out=out, error_flag=flag)
+    torch.cuda.synchronize()
+    assert int(flag.item()) == ssd.DATA_BAD_BLOCK and torch.equal(out[[0, 2]], good[[0, 2]])
+    i["lens"][1] = -7
+    out, lse = call(i)
+    assert (out[1] == 0).all() and (lse[1] == -INF).all() and torch.equal(out[[0, 2]], good[[0, 2]])
+
+
+def test_padded_batch_and_rows_of_nan():
+    """Rows behind the last sequence stay as they were; a query of NaN spoils its own row alone."""
+    i = inputs([600, 50], [2, 3], 8, 2, 128, 16, BF, seed=31)
+    want, want_lse = call(i)
+    q = torch.full((9, 8, 128), NAN, dtype=BF, device="cuda")
+    q[:5] = i["q"]
+    q[1, 5] = NAN
+    plan = ssd.attention_plan(i["lens"], 8, 2, cu_seqlens=i["cu"], total_tokens=9, max_new_tokens=4)
+    out, lse = torch.full_like(q, 3.0), torch.full((9, 8), 4.0, device="cuda")
+    ssd.paged_attention_step(q, i["kc"], i["vc"], i["table"], plan, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert (out[5:] == 3).all() and (lse[5:] == 4).all()
+    assert torch.isnan(out[1, 5]).all()
+    keep = torch.ones(5, 8, dtype=torch.bool)
+    keep[1, 5] = False
+    assert torch.equal(out[:5][keep], want[keep]) and torch.equal(lse[:5][keep], want_lse[keep])
+
+
+def test_many_tokens_of_several_parts():
+    """More tokens than the join has workgroups for: each takes several heads."""
+    i = inputs([2600] * 130, [4] * 130, 8, 1, 64, 16, BF, seed=32)
+    plan = plan_of(i)
+    plan = ssd.dataclasses.replace(plan, max_parts=130 + 400)   # parts of 1024 keys
+    plan = ssd.dataclasses.replace(plan, part_seq=torch.zeros(530, dtype=torch.int32, device="cuda"))
+    ssd._enqueue("ssd_attention_plan_build", i["q"].device, ssd.ctypes.byref(plan.c_struct()))
+    out, lse = call(i, plan=plan)
+    assert plan.part_start[-1].item() == 130 * 3
+    check(i, out, lse, "several parts", only=(0, 64, 129))
+    first = inputs([2600], [4], 8, 1, 64, 16, BF, seed=33)
+    for s in range(0, 130, 13):
+        one = dict(first, q=i["q"][4 * s:4 * s + 4], table=i["table"][s:s + 1], kc=i["kc"], vc=i["vc"])
+        k, v = ref.gather_cache(i["kc"], i["vc"], i["table"][s], 2600)
+        want, err, _, _ = ref.attention(one["q"][3:].cpu(), k, v, 1, p_step=ref.HALF_STEP[BF])
+        ref.check(out[4 * s + 3:4 * s + 4], want, ref.rounded(want, err, BF), f"sequence {s}")
+
+
 def test_scale_strides_and_a_given_workspace():
     i = inputs([400, 30], [1, 1], 6, 3, 64, 32, BF, seed=25, pad=5)
     plan = plan_of(i)

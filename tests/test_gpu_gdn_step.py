@@ -140,6 +140,22 @@ def test_no_decay_full_decay_and_strengths_of_zero_and_one():
     assert torch.isfinite(i["cache"]).all()
 
 
+def test_padded_batch():
+    """Tokens behind the last sequence are not computed, whatever they hold."""
+    i = inputs([2, 1, 4], 4, 2, 64, 24, BF, BF, True, seed=11)
+    before = i["cache"].clone()
+    i["cu"] = torch.tensor([0, 2, 3], dtype=torch.int32).cuda()
+    i["read"], i["v"][3:], i["write"][3:] = i["read"][:2].clone(), float("nan"), 2 ** 31 - 1
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o = torch.full((7, 4, 24), 3.0, dtype=BF, device="cuda")
+    call(i, o=o, error_flag=flag)
+    assert int(flag.item()) == 0 and (o[3:] == 3).all()
+    j = dict(i, write=i["write"][:3])
+    for name in ("q", "k", "v", "gate", "beta"):
+        j[name] = i[name][:3]
+    check(j, before, o[:3], "padded")
+
+
 def test_nothing_to_do():
     i = inputs([0, 0], 2, 1, 64, 16, BF, seed=7)
     before = i["cache"].clone()

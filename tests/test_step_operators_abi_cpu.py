@@ -28,7 +28,7 @@ DELTA = dict(q=FAKE, qs=256, k=FAKE, ks=256, v=FAKE, vs=384, gate=FAKE, gs=4, be
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(dtype=2), DTYPE), (dict(gdtype=-1), DTYPE), (dict(S=-1), SHAPE), (dict(T=-1), SHAPE), (dict(T=4), SHAPE),
+    (dict(dtype=2), DTYPE), (dict(gdtype=-1), DTYPE), (dict(S=-1), SHAPE), (dict(T=-1), SHAPE), (dict(T=4), SHAPE), (dict(T=2 ** 30 + 1, cu=FAKE), SHAPE),
     (dict(H=0), SHAPE), (dict(G=3), SHAPE), (dict(G=0), SHAPE), (dict(dv=0), SHAPE), (dict(dk=0), SHAPE), (dict(slots=-1), SHAPE),
     (dict(eps=NAN), SHAPE), (dict(scale=NAN), SHAPE), (dict(dk=32), UNSUPPORTED), (dict(dk=96), UNSUPPORTED),
     (dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(gate=None), NULL), (dict(beta=None), NULL),
