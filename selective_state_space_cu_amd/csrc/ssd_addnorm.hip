@@ -54,26 +54,27 @@ template <typename Raw> __device__ __forceinline__ void store_streamed(void *p, 
     else *reinterpret_cast<Raw *>(p) = v;
 }
 
-// Where a row's scales come from: none (no 8 bits), a given one, the whole row, groups inside a wave's lanes, larger groups.
+// Where a row's scales come from: none (no 8 bits), a given one, the whole row, groups inside a round of a team's lanes of a
+// wave, larger groups.
 enum Scales { kNoScale, kGiven, kRowScale, kLaneGroups, kWideGroups };
 
 template <typename T, int TEAM, int V, int R, Scales Q>
-__global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void ssd_add_rms_norm_kernel(AddNormArgs a) {
+__global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void ssd_add_rms_norm_kernel(AddNormArgs a) {
     using IO = NormIO<T, V>;
     using Raw = typename IO::Raw;
     struct __attribute__((packed, aligned(4))) Weights { float w[V]; };
-    constexpr int THREADS = TEAM > 256 ? TEAM : 256, SPAN = TEAM * V;
+    constexpr int THREADS = TEAM > 64 ? TEAM : 256, SPAN = TEAM * V, LANES = TEAM < 64 ? TEAM : 64;   // LANES: of a team in a wave
     __shared__ float part[TEAM > 64 ? TEAM / 64 : 1];
-    constexpr int TOPS = Q == kWideGroups ? TEAM * 16 / 128 : TEAM / 64;   // (wide groups have 128 channels at least)
-    __shared__ uint32_t tops[Q == kWideGroups || Q == kRowScale ? THREADS / TEAM * TOPS : 1];
+    constexpr int TOPS = Q == kWideGroups ? TEAM * 16 / 32 : Q == kRowScale && TEAM > 64 ? TEAM / 64 : 1;   // (groups have 32 channels at least)
+    __shared__ uint32_t tops[THREADS / TEAM * TOPS];
     const int lane = threadIdx.x % TEAM, C = a.channels;
-    uint32_t *top = tops + (Q == kWideGroups || Q == kRowScale ? threadIdx.x / TEAM * TOPS : 0);
+    uint32_t *top = tops + threadIdx.x / TEAM * TOPS;
     auto team_sync = [] {   // a wave's LDS operations are in order by themselves
         if constexpr (TEAM > 64) __syncthreads();
         else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
     const int64_t row = (int64_t)blockIdx.x * (THREADS / TEAM) + threadIdx.x / TEAM;
-    if (row >= a.rows) return;   // (whole waves; a team of more than a wave is a workgroup)
+    if (row >= a.rows) return;   // (whole teams; a team of more than a wave is a workgroup)
     const T *x = reinterpret_cast<const T *>(a.x) + row * a.x_stride + lane * V;
     const T *res = reinterpret_cast<const T *>(a.residual) + row * a.residual_stride + lane * V;
     T *res_out = reinterpret_cast<T *>(a.residual_out) + row * a.residual_out_stride + lane * V;
@@ -149,7 +150,7 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void ssd_add_rms_norm_kern
             uint32_t all = 0;
 #pragma unroll
             for (int r = 0; r < R; ++r) all = max(all, m[r]);
-            all = lanes_max(all, 64);
+            all = lanes_max(all, LANES);
             if constexpr (TEAM > 64) {
                 if ((lane & 63) == 0) top[lane >> 6] = all;
                 __syncthreads();
@@ -167,11 +168,11 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void ssd_add_rms_norm_kern
                 if (live(r) && (lane & (lanes - 1)) == 0)
                     a.scales[row * (C / a.group) + (r * SPAN + lane * V) / a.group] = scale[r];
             }
-        } else {   // a group spans several waves
+        } else {   // a group spans several waves, or several rounds of a team
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const uint32_t most = lanes_max(m[r], 64);
-                if (live(r) && (lane & 63) == 0) atomicMax(&top[(r * SPAN + lane * V) / a.group], most);
+                const uint32_t most = lanes_max(m[r], LANES);
+                if (live(r) && (lane & (LANES - 1)) == 0) atomicMax(&top[(r * SPAN + lane * V) / a.group], most);
             }
             team_sync();
             for (int i = lane; i < C / a.group; i += TEAM) a.scales[row * (C / a.group) + i] = scale_of(top[i]);
@@ -203,32 +204,35 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void ssd_add_rms_norm_kern
     }
 }
 
-template <typename T, int TEAM, int V, Scales Q> static hipError_t launch_addnorm_team(const AddNormArgs &a, hipStream_t stream) {
-    constexpr int THREADS = TEAM > 256 ? TEAM : 256, ROWS = THREADS / TEAM;
+template <typename T, int TEAM, int V, Scales Q> static hipError_t launch_addnorm_scales(const AddNormArgs &a, hipStream_t stream) {
+    constexpr int THREADS = TEAM > 64 ? TEAM : 256, ROWS = THREADS / TEAM;
     const int64_t blocks = ((int64_t)a.rows + ROWS - 1) / ROWS;
     if (!fits_grid(blocks, THREADS)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((ssd_add_rms_norm_kernel<T, TEAM, V, 16 / V, Q>), dim3((unsigned)blocks), dim3(THREADS), 0, stream, a);
     return hipGetLastError();
 }
 
-// The smallest team that holds a row with 16 values a lane.
-template <typename T, int V, Scales Q, int TEAM = 64> static hipError_t launch_addnorm_size(const AddNormArgs &a, hipStream_t stream) {
-    if constexpr (TEAM < 1024) {
-        if (a.channels <= TEAM * 16) return launch_addnorm_team<T, TEAM, V, Q>(a, stream);
-        return launch_addnorm_size<T, V, Q, TEAM == 64 ? 256 : 2 * TEAM>(a, stream);
-    } else {
-        static_assert(1024 * 16 >= kNormMaxGroup, "the largest team holds the largest row");
-        return launch_addnorm_team<T, 1024, V, Q>(a, stream);
-    }
+template <typename T, int TEAM, int V> static hipError_t launch_addnorm_team(const AddNormArgs &a, bool e4m3, hipStream_t stream) {
+    constexpr int LANES = TEAM < 64 ? TEAM : 64;
+    if (!e4m3) return launch_addnorm_scales<T, TEAM, V, kNoScale>(a, stream);
+    if (a.scale != nullptr) return launch_addnorm_scales<T, TEAM, V, kGiven>(a, stream);
+    if (a.group == a.channels) return launch_addnorm_scales<T, TEAM, V, kRowScale>(a, stream);
+    if constexpr (V < 8)   // (a group is half a row at most, which 8 values of each lane hold, and 512 channels)
+        if (a.group > LANES * V) return launch_addnorm_scales<T, TEAM, V, kWideGroups>(a, stream);
+    return launch_addnorm_scales<T, TEAM, V, kLaneGroups>(a, stream);
 }
 
-template <typename T, int V> static hipError_t launch_addnorm_v(const AddNormArgs &a, bool e4m3, hipStream_t stream) {
-    if (!e4m3) return launch_addnorm_size<T, V, kNoScale>(a, stream);
-    if (a.scale != nullptr) return launch_addnorm_size<T, V, kGiven>(a, stream);
-    if (a.group == a.channels) return launch_addnorm_size<T, V, kRowScale>(a, stream);
-    if constexpr (V < 8)   // (groups have 512 channels at most)
-        if (a.group > 64 * V) return launch_addnorm_size<T, V, kWideGroups>(a, stream);
-    return launch_addnorm_size<T, V, kLaneGroups>(a, stream);
+// The smallest team that holds a row with 16 values a lane, of 8 lanes at least, or of a wave where values are moved one
+// by one, whose lanes are filled by 64 of them already (2^20 rows of 64 channels bf16: 316 us with a wave each, 85
+// with 8 lanes).
+template <typename T, int V, int TEAM = (V == 1 ? 64 : 8)> static hipError_t launch_addnorm_size(const AddNormArgs &a, bool e4m3, hipStream_t stream) {
+    if constexpr (TEAM < 1024) {
+        if (a.channels <= TEAM * 16) return launch_addnorm_team<T, TEAM, V>(a, e4m3, stream);
+        return launch_addnorm_size<T, V, 2 * TEAM>(a, e4m3, stream);
+    } else {
+        static_assert(1024 * 16 >= kNormMaxGroup, "the largest team holds the largest row");
+        return launch_addnorm_team<T, 1024, V>(a, e4m3, stream);
+    }
 }
 
 // Vectors of 16 bytes where all rows start on such, single values elsewhere.
@@ -240,8 +244,8 @@ template <typename T> static hipError_t launch_addnorm_t(const AddNormArgs &a, b
                             rows * sizeof(T);
     constexpr int V = 16 / sizeof(T);
     const uint64_t codes = e4m3 ? reinterpret_cast<uintptr_t>(a.out) | (uint64_t)a.out_stride : 0;   // V 8-bit values at a time
-    if (starts % 16 == 0 && codes % V == 0) return launch_addnorm_v<T, V>(a, e4m3, stream);
-    return launch_addnorm_v<T, 1>(a, e4m3, stream);
+    if (starts % 16 == 0 && codes % V == 0) return launch_addnorm_size<T, V>(a, e4m3, stream);
+    return launch_addnorm_size<T, 1>(a, e4m3, stream);
 }
 
 // Inputs and the residual that the last-level cache (256 MB) cannot hold are streamed past it (35576 x 4096 bf16 to e4m3 in

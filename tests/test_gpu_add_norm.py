@@ -40,7 +40,9 @@ CASES = [
     (1, 1, F32, True, 0), (1, 64, BF, True, 0), (3, 5, F32, False, 0), (5, 100, BF, True, 3), (2, 4096, BF, True, 0),
     (3, 4100, F32, True, 0), (4, 5120, BF, False, 8), (1, 16384, BF, True, 0), (2, 16383, F32, True, 1), (300, 512, BF, True, 0),
     (7, 2056, BF, True, 4), (33, 96, F32, False, 4), (1000, 128, BF, True, 0), (6, 8192, F32, True, 0), (70, 1031, BF, True, 0),
-    (9, 2048, BF, True, 2), (3, 6144, BF, True, 8), (5, 256, F32, True, 0),
+    (9, 2048, BF, True, 2), (3, 6144, BF, True, 8), (5, 256, F32, True, 0), (131, 64, F32, True, 4), (9, 128, F32, True, 0),
+    (77, 160, BF, False, 8), (5, 1040, BF, True, 0), (3, 2064, F32, True, 4), (4, 512, BF, True, 3), (67, 32, BF, True, 0),
+    (35, 320, F32, True, 0), (6, 768, F32, True, 1), (2, 12288, BF, True, 0), (3, 9728, F32, False, 0),
 ]
 
 
