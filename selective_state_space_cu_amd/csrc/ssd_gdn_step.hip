@@ -13,8 +13,10 @@
 // so that eight rows of a wave's access are whole 128-byte lines, and the two
 // sums over a row take three lane exchanges each. 256 sequences x 32 heads of
 // 128 x 128 take 186 us, 5.8 TB/s (a large copy reaches 5.1). A sequence's tokens
-// follow one another at 1.3 us; loading the next token's inputs ahead made that
-// 1.2 us but cost 4 to 6 % with one to four tokens.
+// follow one another at 1.0 us, all of a token's loads on their way at once;
+// loading the next tokens' inputs ahead, and working out what the state is not
+// needed for beside the state's update, saved no more of that and cost up to 25 %
+// with 8 tokens, by the registers that it takes.
 #include "ssd_elem.hpp"
 
 namespace ssd {
@@ -77,14 +79,26 @@ __global__ __launch_bounds__(kGdnStepThreads) void ssd_gdn_step_kernel(GdnStepAr
                            ? __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(a.cache + rs * slot + head + (int64_t)p * DK + 32 * j))
                            : f32x4{0, 0, 0, 0};
     }
+    const T *kp = reinterpret_cast<const T *>(a.k) + (int64_t)g * DK + 4 * lr, *qp = reinterpret_cast<const T *>(a.q) + (int64_t)g * DK + 4 * lr;
+    const float rate = a.A != nullptr ? a.A[h] : 0.0f, bias = a.A != nullptr && a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f;
     for (int t = t0; t < t1; ++t) {
+        using Four = typename E::Four;
+        Four rk[PIECES], rq[PIECES];
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+            rk[j] = *reinterpret_cast<const Four *>(kp + t * a.k_stride + 32 * j);
+            rq[j] = *reinterpret_cast<const Four *>(qp + t * a.q_stride + 32 * j);
+        }
+        float gate = load_f<GT>(a.gate, t * a.gate_stride + h), beta = load_f<GT>(a.beta, t * a.beta_stride + h), v[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) v[r] = load_f<T>(a.v, t * a.v_stride + (int64_t)h * a.dv + min(p0 + r * GROUPS, a.dv - 1));
+        const int ws = a.write_slot[t];
         f32x4 k[PIECES], q[PIECES];
         float kk = 0.0f, qq = 0.0f, kq = 0.0f;
 #pragma unroll
         for (int j = 0; j < PIECES; ++j) {
-            const int64_t n = (int64_t)g * DK + 32 * j + 4 * lr;
-            k[j] = E::f4(*reinterpret_cast<const typename E::Four *>(reinterpret_cast<const T *>(a.k) + t * a.k_stride + n));
-            q[j] = E::f4(*reinterpret_cast<const typename E::Four *>(reinterpret_cast<const T *>(a.q) + t * a.q_stride + n));
+            k[j] = E::f4(rk[j]);
+            q[j] = E::f4(rq[j]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 kk = fmaf(k[j][i], k[j][i], kk);
@@ -92,9 +106,8 @@ __global__ __launch_bounds__(kGdnStepThreads) void ssd_gdn_step_kernel(GdnStepAr
                 kq = fmaf(k[j][i], q[j][i], kq);
             }
         }
-        float gate = load_f<GT>(a.gate, t * a.gate_stride + h), beta = load_f<GT>(a.beta, t * a.beta_stride + h);
         if (a.A != nullptr) {
-            gate = a.A[h] * softplus_full(gate + (a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f));
+            gate = rate * softplus_full(gate + bias);
             beta = 1.0f / (1.0f + fast_exp2(-beta * kLog2e));
         }
         const float alpha = fast_exp2(gate * kLog2e);
@@ -104,7 +117,6 @@ __global__ __launch_bounds__(kGdnStepThreads) void ssd_gdn_step_kernel(GdnStepAr
             kn = 1.0f / sqrtf(sum8(kk) + a.qk_eps);
             qn *= 1.0f / sqrtf(sum8(qq) + a.qk_eps);
         }
-        const int ws = a.write_slot[t];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int p = p0 + r * GROUPS;
@@ -119,8 +131,7 @@ __global__ __launch_bounds__(kGdnStepThreads) void ssd_gdn_step_kernel(GdnStepAr
             sk = sum8(sk);
             sq = sum8(sq);
             if (p >= a.dv) continue;
-            const float v = load_f<T>(a.v, t * a.v_stride + (int64_t)h * a.dv + p);
-            const float d = beta * (v - alpha * kn * sk) * kn;
+            const float d = beta * fmaf(-(alpha * kn), sk, v[r]) * kn;
             if (lr == 0)
                 reinterpret_cast<T *>(a.o)[t * a.o_stride + (int64_t)h * a.dv + p] = (T)(qn * fmaf(alpha, sq, d * kq));
 #pragma unroll
