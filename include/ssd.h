@@ -591,7 +591,8 @@ ssd_status ssd_gated_delta_step(
  * or the new blocks of the requests up to and with it, refused for lack of
  * blocks or not, are more than *free_count and it needs some
  * (SSD_DATA_NO_BLOCK). A refused request takes no block, its table row stays
- * as it was, its tokens keep their place in the batch, and it gets seq_lens 0,
+ * as it was, its tokens keep their place in the batch (they have none where
+ * num_new itself is refused), and it gets seq_lens 0,
  * read_slot -1 and -1 for its tokens' positions, slots and state slots. A block
  * outside [0, num_blocks) that the table holds gives -1, flagged as
  * SSD_DATA_BAD_BLOCK unless negative. More new tokens in all than total_tokens:
@@ -702,7 +703,8 @@ ssd_status ssd_attention_plan_build(const ssd_attention_plan *plan, void *stream
  *  error_flag      int32 [1] or NULL: a row outside the table sets
  *                  SSD_DATA_BAD_SLOT (the sequence has no keys then); keys past
  *                  the table's last column and blocks outside [0, num_blocks)
- *                  set SSD_DATA_BAD_BLOCK and are left out.
+ *                  set SSD_DATA_BAD_BLOCK and are left out. Blocks of which no
+ *                  token sees a key (before its window) may be anything.
  * Supported: head_dim in {64, 128, 256}, block_size a multiple of 16 up to
  * 2^20, num_blocks * block_size up to 2^31 - 1, nheads % nkvheads == 0.
  * Precision: products' sums and the softmax's maxima and sums in float32. For bf16 the

@@ -301,7 +301,12 @@ __global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(D 
         auto ok = [&](int n) { return (there >> ((KEYS * n + W * g) / W & ~(16 / W - 1)) & 1) != 0; };   // the block of this lane's keys
         const bool masked = key + SK - 1 > all_hi || key + SK > len || key < all_low || ~there != 0;   // uniform
         if (masked) {
-            if (~there != 0 && a.error_flag != nullptr && lane == 0) atomicOr(a.error_flag, SSD_DATA_BAD_BLOCK);
+            if (~there != 0 && a.error_flag != nullptr) {
+                // (a block of which no token sees a key, before the first one's window, may be gone)
+                const bool gone = (uint32_t)now.id >= (uint32_t)a.num_blocks &&
+                                  (a.window == 0 || (int64_t)now.key + 15 + a.window > (int64_t)sp.len - sp.n);
+                if (__any(gone) && lane == 0) atomicOr(a.error_flag, SSD_DATA_BAD_BLOCK);
+            }
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -439,6 +444,7 @@ template <typename T, int D>
 __global__ __launch_bounds__(256) void ssd_attention_join_kernel(AttnArgs a, int blocks_per_token) {
     constexpr int LANES = D / 4, GROUPS = 256 / LANES;
     __shared__ float red[GROUPS][D], red_m[4], red_l[GROUPS];
+    __shared__ int found;
     const int t = blockIdx.x / blocks_per_token;
     int s = t;
     if (a.cu_seqlens != nullptr) {
@@ -449,8 +455,18 @@ __global__ __launch_bounds__(256) void ssd_attention_join_kernel(AttnArgs a, int
         }
         s = lo;
     }
-    const Span sp = span_of(a.cu_seqlens, a.seq_lens, s, a.T, a.max_new, a.window);
-    if (t < sp.t0 || t >= sp.t0 + sp.n) return;
+    Span sp = span_of(a.cu_seqlens, a.seq_lens, s, a.T, a.max_new, a.window);
+    auto has = [t](const Span &r) { return t >= r.t0 && t < r.t0 + r.n; };
+    if (!has(sp)) {   // behind the last sequence, or sequences left out have misled the search: look at each
+        if (threadIdx.x == 0) found = -1;
+        __syncthreads();
+        for (s = threadIdx.x; s < a.S; s += 256)
+            if (has(span_of(a.cu_seqlens, a.seq_lens, s, a.T, a.max_new, a.window))) atomicMax(&found, s);
+        __syncthreads();
+        s = found;
+        if (s < 0) return;
+        sp = span_of(a.cu_seqlens, a.seq_lens, s, a.T, a.max_new, a.window);
+    }
     const int first = a.part_start[s], nparts = a.part_start[s + 1] - first;
     if (nparts <= 1) return;
     const int rows = a.max_new * a.group;

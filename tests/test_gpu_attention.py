@@ -197,6 +197,39 @@ def test_sequences_outside_the_batch_or_too_long_are_left_out():
         assert (out[left] == 3).all() and torch.equal(out[:2], good[:2])
 
 
+def test_sequences_left_out_do_not_hide_others():
+    """The sequences around a damaged one are joined, too, when the places of their tokens do not ascend."""
+    i = inputs([40, 50, 9000], [2, 2, 2], 4, 2, 64, 16, BF, seed=34)
+    good, good_lse = call(i)
+    plan = plan_of(i, max_new=2)
+    assert plan.part_start[3].item() - plan.part_start[2].item() > 1
+    for cu in ([0, 100, 4, 6], [0, -3, 4, 6], [7, 5, 4, 6]):
+        i["cu"] = torch.tensor(cu, dtype=torch.int32).cuda()
+        plan = plan_of(i, max_new=2)
+        assert int(plan.error_flag.item()) == ssd.DATA_BAD_CU_SEQLENS
+        out, lse = torch.full_like(good, 3.0), torch.full_like(good_lse, 4.0)
+        ssd.paged_attention_step(i["q"], i["kc"], i["vc"], i["table"], plan, out=out, lse=lse)
+        torch.cuda.synchronize()
+        assert (out[:4] == 3).all() and (lse[:4] == 4).all()
+        check(i, out, lse, f"{cu}", only=(2,))
+
+
+def test_blocks_before_the_window_may_be_gone():
+    """A table whose blocks before the first token's window have been given back sets no flag; one a token sees does."""
+    for dtype, length, n, window in ((BF, 100, 1, 37), (BF, 100, 3, 30), (F32, 75, 2, 11), (BF, 64, 1, 1), (F32, 100, 4, 97)):
+        i = inputs([length, length], [n, n], 8, 2, 64, 16, dtype, seed=35)
+        good, good_lse = call(i, window)
+        first = length - n - window + 1   # the first key that a token sees
+        i["table"][0, :max(first, 0) // 16] = -1
+        i["table"][1, :max(first, 0) // 16] = i["kc"].shape[0]
+        flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = call(i, window, error_flag=flag)
+        assert int(flag.item()) == 0 and torch.equal(out, good) and torch.equal(lse, good_lse), (length, n, window)
+        i["table"][0, max(first, 0) // 16] = -1
+        call(i, window, error_flag=flag)
+        assert int(flag.item()) == ssd.DATA_BAD_BLOCK, (length, n, window)
+
+
 def test_lengths_past_the_limit_and_below_zero():
     """A sequence of more than 2^30 keys is left out; a negative length counts as none."""
     i = inputs([40, 50, 20], [1] * 3, 4, 2, 64, 16, BF, seed=29)
