@@ -22,11 +22,14 @@
 namespace ssd {
 
 constexpr int kGdnStepThreads = 64;
-// State rows of a lane: 64 or more bytes of states a lane are on their way, and beyond that more lanes do more (1 / 2 / 4
-// rows: dk 128 of 128 sequences x 32 heads x 128 rows 97 / 106 / 106 us, of 16 16.6 / 13.8 / 13.8; dk 64 of 128
-// sequences 57 / 53 / 57, of 16 10.9 / 8.1 / 8.6; dk 256 of 64 x 16 heads x 256 rows 90 / 95 with two). A wave is a
-// workgroup; two or four take 0 to 2 % longer.
-constexpr int gdn_step_rows(int dk) { return dk == 64 ? 2 : 1; }
+// State rows of a lane, from the waves that one row makes. Few waves (two a SIMD): one row, a shorter chain. More: two
+// rows halve the waves to be started and to fetch q, k and the gates, until there are so many (16 a SIMD) that one row's 64
+// bytes of states a lane keep memory busy by themselves; 32 bytes, of dk 64, never do, the 128 of dk 256 always.
+// One / two / four rows, 32 heads x 128 rows, us: dk 128 with 4 sequences 5.7 / 6.2 / 7.2, 8 9.0 / 8.0 / 8.6, 16 16.2 / 14.7 /
+// 13.2, 24 22.0 / 21.8, 32 27.0 / 27.9 / 29.0, 128 95 / 98 / 106; dk 64 with 4 4.8 / 5.1 / 6.4, 8 6.9 / 5.9, 16 11.0 / 8.5 /
+// 8.2, 128 55.8 / 52.4 / 55.3; dk 256 (16 heads x 256 rows) with 4 8.3 / 8.3 / 9.0, 64 90 / 93 / 95. A wave is a workgroup;
+// two or four take 0 to 2 % longer.
+static int gdn_step_rows(int dk, int64_t waves) { return dk <= 128 && waves > 2048 && (dk == 64 || waves < 16384) ? 2 : 1; }
 
 // Sum over the 8 lanes of a row; every lane gets it.
 __device__ __forceinline__ float sum8(float v) {
@@ -145,8 +148,8 @@ __global__ __launch_bounds__(kGdnStepThreads) void ssd_gdn_step_kernel(GdnStepAr
     }
 }
 
-template <typename T, typename GT, int DK> static hipError_t launch_gdn_step_rows(GdnStepArgs a, hipStream_t stream) {
-    constexpr int R = gdn_step_rows(DK), ROWS = kGdnStepThreads / 8 * R;
+template <typename T, typename GT, int DK, int R> static hipError_t launch_gdn_step_rows(GdnStepArgs a, hipStream_t stream) {
+    constexpr int ROWS = kGdnStepThreads / 8 * R;
     a.row_blocks = (a.dv + ROWS - 1) / ROWS;
     const int64_t blocks = (int64_t)a.S * a.H * a.row_blocks;
     if (!fits_grid(blocks, kGdnStepThreads)) return hipErrorInvalidConfiguration;
@@ -156,10 +159,12 @@ template <typename T, typename GT, int DK> static hipError_t launch_gdn_step_row
 }
 
 template <typename T, typename GT> static hipError_t launch_gdn_step_t(const GdnStepArgs &a, int dk, hipStream_t stream) {
+    const int64_t waves = (int64_t)a.S * a.H * ((a.dv + kGdnStepThreads / 8 - 1) / (kGdnStepThreads / 8));
+    const bool two = gdn_step_rows(dk, waves) == 2;
     switch (dk) {
-        case 64: return launch_gdn_step_rows<T, GT, 64>(a, stream);
-        case 128: return launch_gdn_step_rows<T, GT, 128>(a, stream);
-        case 256: return launch_gdn_step_rows<T, GT, 256>(a, stream);
+        case 64: return two ? launch_gdn_step_rows<T, GT, 64, 2>(a, stream) : launch_gdn_step_rows<T, GT, 64, 1>(a, stream);
+        case 128: return two ? launch_gdn_step_rows<T, GT, 128, 2>(a, stream) : launch_gdn_step_rows<T, GT, 128, 1>(a, stream);
+        case 256: return launch_gdn_step_rows<T, GT, 256, 1>(a, stream);
         default: return hipErrorInvalidValue;
     }
 }

@@ -85,6 +85,21 @@ def test_one_token_each_without_cu_seqlens_is_the_same_call():
     assert torch.equal(call(i, single=True), a) and torch.equal(i["cache"], first)
 
 
+@pytest.mark.parametrize("dk,dv,S,dtype", [(64, 20, 24, F32), (128, 20, 24, BF), (128, 9, 260, F32), (64, 130, 10, BF)])
+def test_many_sequences_equal_each_alone(dk, dv, S, dtype):
+    """Batches that take one or two rows a lane: the same bits as each sequence alone, at the float64 bound."""
+    i = inputs([1 + s % 2 for s in range(S)], 32, 16, dk, dv, dtype, seed=41)
+    before = i["cache"].clone()
+    o = call(i)
+    check(i, before, o, f"{S} sequences") if S < 100 else None
+    cu = i["cu"].tolist()
+    for s in (0, 1, S // 2, S - 1):
+        t = slice(cu[s], cu[s + 1])
+        one = dict(i, read=i["read"][s:s + 1], write=i["write"][t], cu=i["cu"][s:s + 2] - cu[s], cache=before.clone(),
+                   **{n: i[n][t] for n in ("q", "k", "v", "gate", "beta")})
+        assert torch.equal(call(one), o[t]) and torch.equal(one["cache"][one["write"].long()], i["cache"][i["write"][t].long()])
+
+
 def test_slots_in_place_fresh_unsaved_and_refused():
     i = inputs([1, 2, 1, 3, 1, 2], 4, 2, 128, 70, BF, F32, False, seed=3)
     slots, cu = i["cache"].shape[0], i["cu"].tolist()
