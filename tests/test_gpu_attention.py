@@ -139,6 +139,20 @@ def test_places_that_a_token_does_not_see():
             assert torch.equal(again[last], out[last]) and torch.equal(again_lse[last], lse[last]), (bad, dtype)
 
 
+@pytest.mark.parametrize("D,dtype,at", [(64, BF, 0), (64, F32, 63), (128, BF, 127), (128, F32, 5), (256, BF, 200), (256, F32, 70)])
+def test_one_value_that_is_not_finite(D, dtype, at):
+    """A single infinity or NaN at a place that some tokens see reaches theirs, in its own place of the head, and no other's."""
+    for bad in (NAN, -INF):
+        i = inputs([150, 39], [4, 2], 8, 2, D, 16, dtype, seed=36)
+        clean, clean_lse = call(i)
+        i["vc"][int(i["table"][0, 147 // 16]), 1, at, 147 % 16] = bad   # tokens 1, 2 and 3 see it, heads 4 .. 7
+        out, lse = call(i)
+        hit = torch.zeros_like(out, dtype=torch.bool)
+        hit[1:4, 4:, at] = True
+        assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse, clean_lse)
+        assert torch.isnan(out[hit]).all() if bad != bad else (out[hit] == bad).all()
+
+
 def test_tokens_that_see_nothing():
     """Empty sequences and tokens before position 0 get zeros and -infinity."""
     i = inputs([0, 2, 40], [1, 4, 2], 4, 2, 64, 16, BF, seed=22)
