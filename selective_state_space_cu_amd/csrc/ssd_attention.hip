@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = 64 * kAttnWaves;
-constexpr int kPartUnit = 256;       // parts are whole multiples of this many keys
+constexpr int kPartUnit = 256;       // parts are multiples of this many keys, a step of each wave (one sequence of 2000: 12.1 us, 15.2 with 512)
 constexpr int kPartEnough = 1024;  // keys of a part that are enough for its workgroup's start and end
 constexpr int kPartsPerSlot = 8;   // workgroups aimed at (2048), over as many as there are CUs
 

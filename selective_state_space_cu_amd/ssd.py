@@ -782,8 +782,8 @@ def step_tables(num_computed: torch.Tensor, num_new: torch.Tensor, block_table: 
     device, i32 = block_table.device, torch.int32
     if block_table.dim() != 2:
         raise ValueError(f"block_table must be (rows, blocks), got {tuple(block_table.shape)}")
-    if block_size < 1:
-        raise ValueError(f"block_size must be positive, got {block_size}")
+    if not 1 <= block_size <= 0x7fffffff:
+        raise ValueError(f"block_size must be 1 .. 2^31 - 1, got {block_size}")
     nseqs, total_tokens = num_computed.shape[0], int(total_tokens)
     if total_tokens < 0:
         raise ValueError(f"total_tokens must not be negative, got {total_tokens}")
@@ -814,8 +814,11 @@ def step_tables(num_computed: torch.Tensor, num_new: torch.Tensor, block_table: 
     read = lens + 4 * nseqs
     pos = read + 4 * nseqs
     one = 4 * total_tokens
+    most = 0x7fffffff // block_size
     if num_blocks is None:
-        num_blocks = 0x7fffffff // block_size
+        num_blocks = most
+    elif not 0 <= num_blocks <= most:
+        raise ValueError(f"num_blocks of {block_size} tokens must be 0 .. {most}, got {num_blocks}")
     _enqueue("ssd_step_tables", device, nseqs, total_tokens, nc.data_ptr(), nn.data_ptr(),
              None if rw is None else rw.data_ptr(), table, table_rows, width, int(block_size), int(num_blocks), free, nfree,
              count, left, cu, lens, pos, pos + one, pos + 2 * one, read, pos + 3 * one, flag)
@@ -886,6 +889,8 @@ def attention_plan(seq_lens: torch.Tensor, num_heads: int, num_kv_heads: int, cu
     device, i32 = seq_lens.device, torch.int32
     if num_heads <= 0 or num_kv_heads <= 0 or num_heads % num_kv_heads:
         raise ValueError(f"num_heads must be a multiple of num_kv_heads, got {num_heads} and {num_kv_heads}")
+    if not 1 <= max_new_tokens <= 64 or not 0 <= window <= 0x7fffffff:
+        raise ValueError(f"max_new_tokens must be 1 .. 64 and window 0 .. 2^31 - 1, got {max_new_tokens} and {window}")
     nseqs = seq_lens.shape[0]
     if cu_seqlens is None:
         if total_tokens not in (None, nseqs):

@@ -221,3 +221,16 @@ def test_bindings_refuse_what_does_not_fit():
                 dict(scales=zeros(3, 2)), dict(out=zeros(3, 64)), dict()):
         with pytest.raises(ValueError):
             ssd.add_rms_norm_e4m3(**dict(dict(x=zeros(3, 64)), **bad))
+
+
+def test_bindings_refuse_numbers_that_do_not_fit_32_bits():
+    i32 = torch.int32
+    for bad in (dict(max_new_tokens=0), dict(max_new_tokens=65), dict(max_new_tokens=2 ** 32 + 1), dict(window=-1),
+                dict(window=2 ** 32 + 5)):
+        with pytest.raises(ValueError, match="max_new_tokens must be"):
+            ssd.attention_plan(zeros(3, dtype=i32), 8, 2, **bad)
+    for bad in (-1, 2 ** 27, 2 ** 32 + 4):
+        with pytest.raises(ValueError, match="num_blocks"):
+            ssd.step_tables(zeros(3, dtype=i32), zeros(3, dtype=i32), zeros(3, 4, dtype=i32), 16, 3, num_blocks=bad)
+    with pytest.raises(ValueError, match="block_size"):
+        ssd.step_tables(zeros(3, dtype=i32), zeros(3, dtype=i32), zeros(3, 4, dtype=i32), 2 ** 32 + 16, 3)
