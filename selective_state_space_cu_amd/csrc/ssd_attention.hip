@@ -35,7 +35,8 @@ namespace {
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = 64 * kAttnWaves;
 constexpr int kPartUnit = 256;       // parts are multiples of this many keys, a step of each wave (one sequence of 2000: 12.1 us, 15.2 with 512)
-constexpr int kPartEnough = 1024;  // keys of a part that are enough for its workgroup's start and end
+constexpr int kPartCost = 1;       // what a part's start and end cost, in such steps
+constexpr int kPlanSearch = 1024;  // sequences among which the best length of the parts is looked for
 constexpr int kPartsPerSlot = 8;   // workgroups aimed at (2048), over as many as there are CUs
 
 template <typename T> struct Mma;
@@ -88,6 +89,8 @@ __device__ __forceinline__ Span span_of(const int32_t *cu, const int32_t *lens, 
 
 __global__ __launch_bounds__(1024) void ssd_attention_plan_kernel(AttnPlanArgs a) {
     __shared__ int64_t wave_sum[16];
+    __shared__ int keys_of[kPlanSearch];
+    __shared__ unsigned long long best;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     auto scan = [&](int64_t v, int64_t &total) {   // inclusive
 #pragma unroll
@@ -110,17 +113,45 @@ __global__ __launch_bounds__(1024) void ssd_attention_plan_kernel(AttnPlanArgs a
         const Span r = span_of(a.cu_seqlens, a.seq_lens, s, a.T, a.max_new, a.window);
         if (r.bad) atomicOr(a.error_flag, SSD_DATA_BAD_CU_SEQLENS);
         if (r.n > 0) keys += r.len - r.lo;
+        if (a.S <= kPlanSearch) keys_of[s] = r.n > 0 ? r.len - r.lo : -1;
     }
+    if (tid == 0) best = ~0ull;
     int64_t total;
     scan(keys, total);
-    // At most max_parts - S parts (many, so that they even out the lengths), but no shorter ones than kPartEnough keys
-    // unless there are too few to give every CU one. One sequence of 30001 keys, 8 kv heads, in 30 / 59 parts a head:
-    // 28.0 / 32.7 us; 64 sequences of 276 K keys in 128 / 192 / 256 / 512 parts and as many more as there are sequences:
-    // 192 / 190 / 190 / 190 us.
-    const int64_t target = a.max_parts - a.S, few = max(target / kPartsPerSlot, (int64_t)1);
-    const int64_t most = (total + target - 1) / target, least = (total + few - 1) / few;
-    const int64_t keys_of = max(most, min(least, (int64_t)kPartEnough));
-    const int part = (int)min(max((keys_of + kPartUnit - 1) / kPartUnit * kPartUnit, (int64_t)kPartUnit), (int64_t)kMostKeys);
+    // At most max_parts - S parts (`least` units each, or more) and, by their remainders, one a sequence more.
+    constexpr int kMostUnits = kMostKeys / kPartUnit;
+    const uint32_t target = a.max_parts - a.S;
+    const int64_t most = (total >> 31) == 0 ? ((uint32_t)total + target - 1) / target : (total + target - 1) / target;
+    const int least = (int)min(max((most + kPartUnit - 1) / kPartUnit, (int64_t)1), (int64_t)kMostUnits), step = (7 * least + 63) / 64;
+    auto units = [&](int candidate) { return min(least + candidate * step, kMostUnits); };
+    // Of 64 lengths up to 8 times the shortest (or 64 units), the one by which the fullest CU has least to do: its workgroups, times their
+    // steps and one more for start and end. One workgroup a CU reads a little slower than two (an eighth more), and
+    // short parts even out what this leaves out (1/64 for each time the shortest). 8 kv heads of 128 bf16, parts of 1024
+    // keys or, with more of them than 8 for each CU, longer / of this length, us: 30000 keys 27.9 / 27.7 (1024), 4
+    // sequences of 10000 39.4 / 33.2 (1280), 100000 83.3 / 76.1, 64 of 48 to 7900 200 / 201 (1280 both), 32 with a window of
+    // 4096 104 / 99, 8 tokens each of 16 of 3000 (64 heads, four tiles) 90 / 73.
+    // (Not looked for where the shortest ones leave no CU two workgroups; the plan then takes 5 us instead of 8 to 11.)
+    const bool search = a.S <= kPlanSearch && kPartsPerSlot * (total / kPartUnit + a.S) > target;
+    if (search) {
+        int parts[4] = {};
+        for (int s = lane; s < a.S; s += 64)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                // (whole units over units: short operands)
+                const uint32_t keys = keys_of[s], of = (keys + kPartUnit - 1) / kPartUnit, k = units(4 * wave + c);
+                parts[c] += keys_of[s] < 0 ? 0 : max((int)((of + k - 1) / k), 1);
+            }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int x = 32; x >= 1; x >>= 1) parts[c] += __shfl_xor(parts[c], x);
+            const uint32_t k = units(4 * wave + c), rounds = ((uint32_t)kPartsPerSlot * parts[c] + target - 1) / target;
+            const uint64_t cost = (uint64_t)(rounds == 1 ? 9 : 8 * rounds) * ((k + kPartCost) * (64 + k / least));
+            if (lane == 0) atomicMin(&best, (unsigned long long)(cost << 6 | (uint64_t)(4 * wave + c)));
+        }
+        __syncthreads();
+    }
+    const int part = kPartUnit * units(search ? (int)(best & 63) : 0);
     int64_t carry = 0;
     for (int base = 0; base < a.S; base += 1024) {
         const int s = base + tid;

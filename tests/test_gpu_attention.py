@@ -100,7 +100,10 @@ def test_long_sequences_in_many_parts_equal_float64():
 
 def test_plan_covers_every_key_once():
     for seed, (lengths, counts, window) in enumerate([([1, 0, 5000, 128, 129], [1] * 5, 0), ([70000, 3], [1, 1], 0),
-                                                      ([4000, 10, 0, 300], [4, 4, 2, 0], 1000), ([0, 0], [0, 0], 0)]):
+                                                      ([4000, 10, 0, 300], [4, 4, 2, 0], 1000), ([0, 0], [0, 0], 0),
+                                                      ([3 * s for s in range(1500)], [1] * 1500, 0), ([2 ** 30] * 1024, [1] * 1024, 0),
+                                                      ([2 ** 30 - s for s in range(1025)], [2] * 1025, 0),
+                                                      ([40000, 39999, 17] * 9, [3, 1, 2] * 9, 4096)]):
         lens, cu = torch.tensor(lengths, dtype=torch.int32).cuda(), torch.tensor([0] + counts).cumsum(0).to(torch.int32).cuda()
         plan = ssd.attention_plan(lens, 8, 2, cu_seqlens=cu, total_tokens=sum(counts), max_new_tokens=4, window=window)
         part, starts, seqs = int(plan.part_keys.item()), plan.part_start.tolist(), plan.part_seq.tolist()
@@ -287,11 +290,10 @@ def test_many_tokens_of_several_parts():
     """More tokens than the join has workgroups for: each takes several heads."""
     i = inputs([2600] * 130, [4] * 130, 8, 1, 64, 16, BF, seed=32)
     plan = plan_of(i)
-    plan = ssd.dataclasses.replace(plan, max_parts=130 + 400)   # parts of 1024 keys
-    plan = ssd.dataclasses.replace(plan, part_seq=torch.zeros(530, dtype=torch.int32, device="cuda"))
+    plan = ssd.dataclasses.replace(plan, max_parts=130 + 2000, part_seq=torch.zeros(2130, dtype=torch.int32, device="cuda"))
     ssd._enqueue("ssd_attention_plan_build", i["q"].device, ssd.ctypes.byref(plan.c_struct()))
     out, lse = call(i, plan=plan)
-    assert plan.part_start[-1].item() == 130 * 3
+    assert plan.part_start[-1].item() == 130 * 3   # parts of 1024 keys
     check(i, out, lse, "several parts", only=(0, 64, 129))
     first = inputs([2600], [4], 8, 1, 64, 16, BF, seed=33)
     for s in range(0, 130, 13):
