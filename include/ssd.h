@@ -656,7 +656,7 @@ typedef struct {
     int32_t total_tokens;       /* [host] T: rows of q */
     int32_t max_new_tokens;     /* [host] most tokens of a sequence, 1 .. 64 */
     int32_t window;             /* [host] keys a token sees, its own among them; 0: all */
-    int32_t max_parts;          /* [host] capacity, > S; max_parts - S parts are aimed at */
+    int32_t max_parts;          /* [host] capacity, > S; max_parts - S: ssd_paged_attention_parts of the layers */
     const int32_t *seq_lens;    /* in  [S] keys of each sequence, its new tokens' among them */
     const int32_t *cu_seqlens;  /* in  [S+1] tokens as in ssd_gated_delta_step, or NULL: one each (T == S) */
     int32_t *part_start;        /* out [S+1] first part of each sequence; [S] = number of parts */
@@ -722,7 +722,10 @@ ssd_status ssd_paged_attention_step(
     int32_t table_rows, int32_t max_blocks, const int32_t *rows, int32_t num_blocks, int32_t block_size, void *out,
     int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes, int32_t *error_flag, void *stream);
 
-/* Parts to aim at (max_parts - nseqs of a plan) so that a call with these heads fills the GPU. */
+/*
+ * Parts that give each CU eight workgroups of a call with these heads: what max_parts - nseqs of a plan should be. A
+ * plan cuts no more (and one a sequence by their remainders), but fewer, longer ones where they share the work better.
+ */
 int32_t ssd_paged_attention_parts(int32_t max_new_tokens, int32_t nheads, int32_t nkvheads);
 
 /* Workspace bytes that ssd_paged_attention_step needs for a plan of max_parts and max_new_tokens. */
