@@ -470,7 +470,8 @@ __global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(D 
         for (int w = 0; w < kAttnWaves; ++w) best = fmaxf(best, wave_m[w][row]);
         f32x4 v{0, 0, 0, 0};
         for (int w = 0; w < kAttnWaves; ++w) {
-            sum += best == -INFINITY ? 0.0f : wave_l[w][row] * fast_exp2(wave_m[w][row] - best);
+            // (where no product is above -infinity the waves' sums are 0, or NaN if one is NaN, which no maximum shows)
+            sum += best == -INFINITY ? wave_l[w][row] : wave_l[w][row] * fast_exp2(wave_m[w][row] - best);
             v += *reinterpret_cast<const f32x4 *>(red + red_at(w, row, d / 4));
         }
         if (nparts == 1) {
