@@ -84,6 +84,9 @@ ssd_status check_plan(const ssd_attention_plan *p) {
     return SSD_OK;
 }
 
+// A window of 2^30 keys is none (sequences have no more), so the kernels' positions less a window stay in 32 bits.
+int32_t attention_window(const ssd_attention_plan *p) { return p->window >= (1 << 30) ? 0 : p->window; }
+
 // Tiles of 16 rows (tokens x query heads of a kv head).
 int32_t attention_tiles(int32_t max_new_tokens, int32_t group) {
     return (int32_t)(((int64_t)max_new_tokens * group + 15) / 16);
@@ -590,7 +593,7 @@ ssd_status ssd_attention_plan_build(const ssd_attention_plan *plan, void *stream
     ssd::AttnPlanArgs a{};
     a.seq_lens = plan->seq_lens; a.cu_seqlens = plan->cu_seqlens; a.part_start = plan->part_start;
     a.part_seq = plan->part_seq; a.part_keys = plan->part_keys; a.error_flag = plan->error_flag;
-    a.S = plan->nseqs; a.T = plan->total_tokens; a.max_new = plan->max_new_tokens; a.window = plan->window;
+    a.S = plan->nseqs; a.T = plan->total_tokens; a.max_new = plan->max_new_tokens; a.window = attention_window(plan);
     a.max_parts = plan->max_parts;
     return ssd::launch_attention_plan(a, static_cast<hipStream_t>(stream)) == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
@@ -643,7 +646,7 @@ ssd_status ssd_paged_attention_step(const void *q, int64_t q_stride, const void 
     a.out = out; a.lse = lse;
     a.part_o = static_cast<float *>(workspace); a.part_ml = a.part_o + parts * head_dim;
     a.error_flag = error_flag; a.scale_log2 = scale * 1.4426950408889634f;
-    a.S = plan->nseqs; a.T = plan->total_tokens; a.max_new = plan->max_new_tokens; a.window = plan->window;
+    a.S = plan->nseqs; a.T = plan->total_tokens; a.max_new = plan->max_new_tokens; a.window = attention_window(plan);
     a.max_parts = plan->max_parts; a.Hq = nheads; a.Hkv = nkvheads; a.group = nheads / nkvheads;
     a.tiles = attention_tiles(plan->max_new_tokens, a.group);
     // no cache, no table: no keys
