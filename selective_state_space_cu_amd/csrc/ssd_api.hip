@@ -88,9 +88,7 @@ ssd_status check_plan(const ssd_attention_plan *p) {
 int32_t attention_window(const ssd_attention_plan *p) { return p->window >= (1 << 30) ? 0 : p->window; }
 
 // Tiles of 16 rows (tokens x query heads of a kv head).
-int32_t attention_tiles(int32_t max_new_tokens, int32_t group) {
-    return (int32_t)(((int64_t)max_new_tokens * group + 15) / 16);
-}
+int64_t attention_tiles(int32_t max_new_tokens, int32_t group) { return ((int64_t)max_new_tokens * group + 15) / 16; }
 
 // What the two norms with a residual ask of their shared arguments.
 ssd_status check_add_norm(const ssd::AddNormArgs &a, ssd_dtype in_dtype) {
@@ -600,7 +598,7 @@ ssd_status ssd_attention_plan_build(const ssd_attention_plan *plan, void *stream
 
 int32_t ssd_paged_attention_parts(int32_t max_new_tokens, int32_t nheads, int32_t nkvheads) {
     if (max_new_tokens <= 0 || nheads <= 0 || nkvheads <= 0 || nheads % nkvheads != 0) return 0;
-    const int64_t per_part = (int64_t)nkvheads * attention_tiles(max_new_tokens, nheads / nkvheads);
+    const int64_t per_part = nkvheads * attention_tiles(max_new_tokens, nheads / nkvheads);
     return (int32_t)((ssd::kAttnWorkgroups + per_part - 1) / per_part);
 }
 
@@ -648,7 +646,7 @@ ssd_status ssd_paged_attention_step(const void *q, int64_t q_stride, const void 
     a.error_flag = error_flag; a.scale_log2 = scale * 1.4426950408889634f;
     a.S = plan->nseqs; a.T = plan->total_tokens; a.max_new = plan->max_new_tokens; a.window = attention_window(plan);
     a.max_parts = plan->max_parts; a.Hq = nheads; a.Hkv = nkvheads; a.group = nheads / nkvheads;
-    a.tiles = attention_tiles(plan->max_new_tokens, a.group);
+    a.tiles = (int32_t)attention_tiles(plan->max_new_tokens, a.group);   // (64 tokens of 2^26 / 64 heads at most)
     // no cache, no table: no keys
     a.table_rows = num_blocks > 0 && max_blocks > 0 ? table_rows : 0;
     a.max_blocks = max_blocks; a.num_blocks = num_blocks; a.block = block_size;

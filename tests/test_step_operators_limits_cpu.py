@@ -1,0 +1,24 @@
+"""Sizes at and past the ends of what the decode step's calls take, on the CPU."""
+import os
+
+import pytest
+import torch
+
+from selective_state_space_cu_amd import ssd
+
+pytestmark = pytest.mark.skipif(not os.path.exists(ssd.LIB_PATH), reason="libssd.so not built")
+
+I32 = torch.int32
+
+
+def zeros(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def test_parts_of_any_number_of_heads():
+    """Rows (tokens x heads) past 32 bits: one part fills the GPU."""
+    parts = ssd.load_library().ssd_paged_attention_parts
+    for tokens, heads, kv in ((64, 2 ** 30, 1), (64, 2 ** 31 - 1, 1), (2 ** 31 - 1, 2 ** 30, 2 ** 29), (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1),
+                              (2 ** 31 - 1, 16, 1)):
+        assert parts(tokens, heads, kv) == 1
+    assert parts(64, 64, 1) == 8 and parts(1, 1, 1) == 2048
