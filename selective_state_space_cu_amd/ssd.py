@@ -785,8 +785,8 @@ def step_tables(num_computed: torch.Tensor, num_new: torch.Tensor, block_table: 
     if not 1 <= block_size <= 0x7fffffff:
         raise ValueError(f"block_size must be 1 .. 2^31 - 1, got {block_size}")
     nseqs, total_tokens = num_computed.shape[0], int(total_tokens)
-    if total_tokens < 0:
-        raise ValueError(f"total_tokens must not be negative, got {total_tokens}")
+    if not 0 <= total_tokens <= 0x7fffffff:
+        raise ValueError(f"total_tokens must be 0 .. 2^31 - 1, got {total_tokens}")
     table_rows, width = block_table.shape
     nc = _slots(num_computed, "num_computed", device, nseqs)
     nn = _slots(num_new, "num_new", device, nseqs)
@@ -887,8 +887,8 @@ def attention_plan(seq_lens: torch.Tensor, num_heads: int, num_kv_heads: int, cu
     seq_lens (S,): keys of each sequence, its new tokens' among them. Without cu_seqlens every sequence has one new token;
     with cu_seqlens (S+1,) pass total_tokens and max_new_tokens (the most of a sequence, up to 64)."""
     device, i32 = seq_lens.device, torch.int32
-    if num_heads <= 0 or num_kv_heads <= 0 or num_heads % num_kv_heads:
-        raise ValueError(f"num_heads must be a multiple of num_kv_heads, got {num_heads} and {num_kv_heads}")
+    if not 0 < num_heads <= 0x7fffffff or num_kv_heads <= 0 or num_heads % num_kv_heads:
+        raise ValueError(f"num_heads must be a multiple of num_kv_heads and at most 2^31 - 1, got {num_heads} and {num_kv_heads}")
     if not 1 <= max_new_tokens <= 64 or not 0 <= window <= 0x7fffffff:
         raise ValueError(f"max_new_tokens must be 1 .. 64 and window 0 .. 2^31 - 1, got {max_new_tokens} and {window}")
     nseqs = seq_lens.shape[0]
@@ -896,8 +896,8 @@ def attention_plan(seq_lens: torch.Tensor, num_heads: int, num_kv_heads: int, cu
         if total_tokens not in (None, nseqs):
             raise ValueError(f"{total_tokens} tokens of {nseqs} sequences need cu_seqlens")
         total_tokens = nseqs
-    elif total_tokens is None:
-        raise ValueError("pass total_tokens with cu_seqlens")
+    elif total_tokens is None or not 0 <= total_tokens <= 0x7fffffff:
+        raise ValueError(f"pass total_tokens, 0 .. 2^31 - 1, with cu_seqlens, got {total_tokens}")
     lens = _slots(seq_lens, "seq_lens", device, nseqs)
     cu = None if cu_seqlens is None else _slots(cu_seqlens, "cu_seqlens", device, nseqs + 1)
     parts = nseqs + int((_lib or load_library()).ssd_paged_attention_parts(int(max_new_tokens), num_heads, num_kv_heads))

@@ -22,3 +22,18 @@ def test_parts_of_any_number_of_heads():
                               (2 ** 31 - 1, 16, 1)):
         assert parts(tokens, heads, kv) == 1
     assert parts(64, 64, 1) == 8 and parts(1, 1, 1) == 2048
+
+
+@pytest.mark.parametrize("total", [-1, 2 ** 31, 2 ** 32 + 3])
+def test_bindings_refuse_tokens_past_32_bits(total):
+    """Before anything of that size is allocated."""
+    with pytest.raises(ValueError, match="total_tokens"):
+        ssd.step_tables(zeros(3, dtype=I32), zeros(3, dtype=I32), zeros(3, 4, dtype=I32), 16, total)
+    with pytest.raises(ValueError, match="total_tokens"):
+        ssd.attention_plan(zeros(3, dtype=I32), 8, 2, cu_seqlens=zeros(4, dtype=I32), total_tokens=total)
+
+
+@pytest.mark.parametrize("heads,kv", [(2 ** 31, 8), (2 ** 32 + 8, 8), (2 ** 32 + 8, 2 ** 32 + 8)])
+def test_bindings_refuse_heads_past_32_bits(heads, kv):
+    with pytest.raises(ValueError, match="num_heads must be"):
+        ssd.attention_plan(zeros(3, dtype=I32), heads, kv)
