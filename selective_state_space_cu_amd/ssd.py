@@ -924,7 +924,7 @@ def paged_attention_step(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     if plan._device != device:
         raise ValueError(f"the plan must be on {device}, got {plan._device}")
     heads = shape[1]
-    if heads % kv_heads:
+    if kv_heads == 0 or heads % kv_heads:
         raise ValueError(f"q's heads must be a multiple of the cache's {kv_heads}, got {heads}")
     if block_table.dim() != 2:
         raise ValueError(f"block_table must be (rows, blocks), got {tuple(block_table.shape)}")
@@ -994,13 +994,13 @@ def add_rms_norm_e4m3(x: torch.Tensor, weight: Optional[torch.Tensor] = None, re
     head, residual_out, res = _add_norm_inputs(x, weight, residual, residual_out)
     device, (rows, channels), f32 = x.device, x.shape, torch.float32
     group = int(group) or channels
-    if group < 0 or channels % max(group, 1):
+    if group <= 0 or channels % group:
         raise ValueError(f"group must divide the {channels} channels, got {group}")
     if scale is not None and scales is not None:
         raise ValueError("scales is written only without a given scale")
     given = _whole(scale, "scale", device, f32, (1,))
     if scale is None and scales is None:
-        scales = torch.empty(rows, channels // max(group, 1), dtype=f32, device=device)
+        scales = torch.empty(rows, channels // group, dtype=f32, device=device)
     made = None if scales is None else _whole(scales, "scales", device, f32, (rows, channels // group))
     if out is None:
         out = torch.empty(rows, channels, dtype=torch.float8_e4m3fn, device=device)

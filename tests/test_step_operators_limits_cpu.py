@@ -37,3 +37,12 @@ def test_bindings_refuse_tokens_past_32_bits(total):
 def test_bindings_refuse_heads_past_32_bits(heads, kv):
     with pytest.raises(ValueError, match="num_heads must be"):
         ssd.attention_plan(zeros(3, dtype=I32), heads, kv)
+
+
+def test_bindings_refuse_caches_without_heads_and_rows_without_channels():
+    plan = ssd.AttentionPlan(3, 3, 1, 0, 20, *(zeros(24, dtype=I32) for _ in range(6)))
+    with pytest.raises(ValueError, match="heads must be a multiple"):
+        ssd.paged_attention_step(zeros(3, 4, 64), zeros(4, 0, 16, 64), zeros(4, 0, 64, 16), zeros(3, 4, dtype=I32), plan)
+    for group in (0, 32):
+        with pytest.raises(ValueError, match="GPU" if group else "group must divide"):
+            ssd.add_rms_norm_e4m3(zeros(3, 0), group=group)
