@@ -221,7 +221,7 @@ hipError_t launch_step_tables(const TablesArgs &a, hipStream_t stream) {
     const bool one = a.T <= kTablesOneLaunch && a.S <= kTablesThreads;
     hipLaunchKernelGGL(ssd_step_tables_kernel, dim3(1), dim3(kTablesThreads), 0, stream, a, one ? a.T : 0);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || one) return e;
+    if (e != hipSuccess || one || a.T == 0) return e;   // (no tokens, no maps)
     hipLaunchKernelGGL(ssd_token_maps_kernel, dim3((unsigned)((a.T + 255) / 256)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
