@@ -750,8 +750,9 @@ size_t ssd_paged_attention_workspace_size(int32_t max_parts, int32_t max_new_tok
  *  out             1 byte each, (rows, channels), rows out_stride bytes apart
  *  scale           float32 [1] on the device: one given scale; or NULL:
  *  scales          float32 (rows, channels/group), written: max |n| / 448 over
- *                  each `group` consecutive channels, 1 where all are zero. A
- *                  NaN among them makes the scale NaN. group == channels: one a row.
+ *                  each `group` consecutive channels (at least 2^-149, the
+ *                  smallest float32), 1 where all are zero. A NaN among them
+ *                  makes the scale NaN. group == channels: one a row.
  * Supported: channels 1 .. 16384; group == channels, or 32, 64, 128, 256 or 512
  * where channels is a multiple of it; eps >= 0.
  * Precision: float32; the norm takes r as it is before its rounding to

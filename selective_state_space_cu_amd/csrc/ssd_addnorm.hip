@@ -141,7 +141,10 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void ssd_add_rms_norm_kerne
 #pragma unroll
             for (int i = 0; i < V; ++i) m[r] = max(m[r], __float_as_uint(v[r * V + i]) & 0x7fffffffu);
         }
-        auto scale_of = [](uint32_t bits) { return bits == 0 ? 1.0f : __uint_as_float(bits) * (1.0f / kE4m3Max); };
+        // (a scale that would round to 0, whose reciprocal makes NaN of zeros, is the smallest value above it)
+        auto scale_of = [](uint32_t bits) {
+            return bits == 0 ? 1.0f : __uint_as_float(max(__float_as_uint(__uint_as_float(bits) * (1.0f / kE4m3Max)), 1u));
+        };
         float scale[R];
         if constexpr (Q == kGiven) {
 #pragma unroll

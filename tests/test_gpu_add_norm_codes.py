@@ -1,0 +1,45 @@
+"""The 8-bit output's codes where a rounding border decides: e4m3(n / scale) of the float32 quotient, scales max |n| / 448.
+
+Rows of +-1 have a mean square of 1, so with eps 0 the norm is the weights themselves, and every expected scale and code is
+exact."""
+import pytest
+import torch
+
+from selective_state_space_cu_amd import ssd
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+BF, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+INF, NAN = float("inf"), float("nan")
+
+
+def signs(rows, c, dtype, seed):
+    r = torch.Generator().manual_seed(seed)
+    return (2.0 * torch.randint(0, 2, (rows, c), generator=r) - 1).to(dtype)
+
+
+def codes(quotient):
+    """What the codes of float32 quotients stand for (NaN stays NaN)."""
+    return quotient.clamp(-448, 448).to(E4M3).float()
+
+
+def call(x, w, **kw):
+    out, scales, _ = ssd.add_rms_norm_e4m3(x.cuda(), weight=w.cuda(), eps=0.0, **kw)
+    torch.cuda.synchronize()
+    return out.float().cpu(), scales.cpu()
+
+
+def same(a, b):
+    return torch.equal(torch.nan_to_num(a, nan=1e9), torch.nan_to_num(b, nan=1e9))
+
+
+@pytest.mark.parametrize("dtype,c,group", [(BF, 256, 64), (F32, 256, 64), (F32, 1024, 512), (BF, 1024, 0), (F32, 31, 0)])
+def test_groups_too_small_for_their_quotient_by_448(dtype, c, group):
+    """Non-zero values below 448 x 2^-150, whose scale would round to 0: it is the smallest there is, and zeros stay zeros."""
+    size = group or c
+    w = torch.arange(c) % 25 * 2.0 ** -149   # 0 .. 24 steps
+    x = signs(3, c, dtype, 65)
+    out, scales = call(x, w, group=group)
+    assert (scales == 2.0 ** -149).all() and scales.shape == (3, c // size)
+    assert same(out, codes((torch.arange(c) % 25).float()) * x.float())
