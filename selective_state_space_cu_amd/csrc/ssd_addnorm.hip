@@ -188,7 +188,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void ssd_add_rms_norm_kerne
         for (int r = 0; r < R; ++r) {
             if (!live(r)) continue;
             float *f = v + r * V;
-            if (scale[r] < 0x1p-100f) {   // whose reciprocal may be infinite
+            if (fabsf(scale[r]) < 0x1p-100f) {   // whose reciprocal may be infinite
                 scale[r] *= 0x1p100f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) f[i] *= 0x1p100f;

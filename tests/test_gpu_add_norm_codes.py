@@ -43,3 +43,13 @@ def test_groups_too_small_for_their_quotient_by_448(dtype, c, group):
     out, scales = call(x, w, group=group)
     assert (scales == 2.0 ** -149).all() and scales.shape == (3, c // size)
     assert same(out, codes((torch.arange(c) % 25).float()) * x.float())
+
+
+@pytest.mark.parametrize("scale", [-0.25, -3.0, -2.0 ** 33, 2.0 ** 33, -2.0 ** -110, 2.0 ** -130, 2.0 ** 126, 0.0, INF, NAN])
+def test_given_scales_of_any_sign_and_size(scale):
+    w = torch.tensor([0.0, 1.0, 25.0, 2.0 ** 40, 3 * 2.0 ** 39, 2.0 ** 127, 7 * 2.0 ** -149, 2.0 ** -105, INF, NAN, 0.3, 2.0 ** 31,
+                      2.0 ** 128 - 2.0 ** 104, 2.0 ** -140, 1e-30, 1e30])
+    x = signs(2, 16, F32, 64)
+    given = torch.tensor([scale])
+    out, _ = call(x, w, scale=given.cuda())
+    assert same(out, codes(w / given * x))
