@@ -756,7 +756,8 @@ size_t ssd_paged_attention_workspace_size(int32_t max_parts, int32_t max_new_tok
  * Supported: channels 1 .. 16384; group == channels, or 32, 64, 128, 256 or 512
  * where channels is a multiple of it; eps >= 0.
  * Precision: float32; the norm takes r as it is before its rounding to
- * residual_out; one rounding of each output.
+ * residual_out; one rounding of each output, in 8 bits of the float32 quotient
+ * n / scale.
  * Errors: SSD_ERR_DTYPE, SSD_ERR_SHAPE (sizes, strides, alignment to the
  * element, eps), SSD_ERR_UNSUPPORTED (channels, group), SSD_ERR_NULL_ARG,
  * SSD_ERR_HIP.

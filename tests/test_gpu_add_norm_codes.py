@@ -53,3 +53,42 @@ def test_given_scales_of_any_sign_and_size(scale):
     given = torch.tensor([scale])
     out, _ = call(x, w, scale=given.cuda())
     assert same(out, codes(w / given * x))
+
+
+def ties():
+    """Values half way between two codes: 2^e (2 k + 1) / 16 for k = 8 .. 15, and those below the smallest normal code."""
+    normal = [2.0 ** e * (2 * k + 1) / 16 for e in range(-6, 9) for k in range(8, 16)]
+    return torch.tensor([v for v in normal if v < 448] + [(2 * k + 1) * 2.0 ** -10 for k in range(8)])
+
+
+@pytest.mark.parametrize("dtype,odd", [(BF, False), (F32, False), (BF, True), (F32, True)])
+def test_exact_ties_under_a_given_scale(dtype, odd):
+    """n = tie x scale without a rounding, so n / scale is the tie itself, which goes to the even code."""
+    r = torch.Generator().manual_seed(61)
+    t = ties()
+    t = t[:len(t) // 8 * 8 - (3 if odd else 0)]
+    x = signs(3, t.numel(), dtype, 62)
+    for k in range(60):
+        scale = torch.randint(1 << 15, 1 << 16, (1,), generator=r).float() * 2.0 ** (k % 40 - 35)   # 16 bits, t has 5
+        w = t * scale
+        assert torch.equal(w.double(), t.double() * scale.double())
+        out, _ = call(x, w, scale=scale.cuda())
+        assert same(out, codes(t) * x.float()), float(scale)
+
+
+CASES = [(2, 4096, 0, BF), (3, 4096, 128, BF), (3, 1024, 512, F32), (2, 512, 64, F32), (5, 320, 32, BF), (2, 1031, 0, BF), (4, 96, 32, F32),
+         (2, 16384, 256, BF), (2, 9728, 256, F32)]
+
+
+@pytest.mark.parametrize("rows,c,group,dtype", CASES)
+def test_scales_and_codes_are_those_of_the_float32_quotients(rows, c, group, dtype):
+    w = torch.randn(c, generator=torch.Generator().manual_seed(c)).abs() * 3
+    x = signs(rows, c, dtype, 63)
+    size = group or c
+    want = w.view(-1, size).amax(1) / 448
+    out, scales = call(x, w, group=group)
+    assert torch.equal(scales, want.expand(rows, -1))
+    assert same(out, codes(w / want.repeat_interleave(size)) * x.float())
+    given = torch.tensor([0.0171])
+    out, _ = call(x, w, scale=given.cuda())
+    assert same(out, codes(w / given) * x.float())
