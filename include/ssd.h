@@ -584,6 +584,15 @@ ssd_status ssd_gated_delta_step(
  *                  write_slot of ssd_gated_delta_step, which so keeps the state
  *                  at every block's end and after the last token
  * Tokens at and past cu_seqlens[nseqs] get -1 everywhere (a padded batch).
+ * Where tokens of an earlier step were not kept (speculated ones that were not
+ * accepted) and num_computed falls back, the caller sees to what the lengths
+ * alone do not show. What row rows[s] has from column
+ * ceil(num_computed / block_size) on is overwritten when blocks are taken, so the
+ * blocks of the tokens given up go back to the free list first, or they are
+ * in no list any more. And read_slot and state_slot keep one state a block,
+ * its latest: speculated tokens take slots of the caller's own in
+ * ssd_gated_delta_step, one a token, and the next step reads that of the last
+ * one accepted.
  * A request is refused, with its bit set in error_flag, when its counts are
  * negative, its num_new exceeds total_tokens or its length 2^31-1
  * (SSD_DATA_BAD_CU_SEQLENS), its row is outside the table (SSD_DATA_BAD_SLOT),

@@ -778,7 +778,9 @@ def step_tables(num_computed: torch.Tensor, num_new: torch.Tensor, block_table: 
     the caches and new in this step; total_tokens: their sum, or the padded batch's tokens. block_table int32 (table rows,
     blocks) holds request s in row rows[s] (s without rows) and gets the new blocks, taken from the end of
     free_blocks[:free_count]; what is left is written to free_count_out (a new tensor unless given; free_count itself
-    updates it in place). num_blocks bounds the table's entries (2^31 - 1 slots unless given)."""
+    updates it in place). num_blocks bounds the table's entries (2^31 - 1 slots unless given). Tokens that are given up
+    after a step: their blocks, from column ceil(num_computed / block_size) on, go back to the free list before the next
+    call, which overwrites those entries; states after such tokens need slots of the caller's own (see ssd_step_tables)."""
     device, i32 = block_table.device, torch.int32
     if block_table.dim() != 2:
         raise ValueError(f"block_table must be (rows, blocks), got {tuple(block_table.shape)}")
