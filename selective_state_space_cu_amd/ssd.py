@@ -878,6 +878,9 @@ class AttentionPlan:
                   self.error_flag.data_ptr())
         object.__setattr__(self, "_c", c)
         object.__setattr__(self, "_device", self.part_start.device)
+        sizes = ((self.seq_lens, self.nseqs), (self.cu_seqlens, self.nseqs + 1), (self.part_start, self.nseqs + 1),
+                 (self.part_seq, self.max_parts), (self.part_keys, 1), (self.error_flag, 1))
+        object.__setattr__(self, "_fits", all(t is None or t.numel() >= n for t, n in sizes))
 
     def c_struct(self) -> _Plan:
         return self._c
@@ -925,6 +928,8 @@ def paged_attention_step(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
         raise ValueError(f"q must be ({plan.total_tokens}, heads, {dim}), got {tuple(shape)}")
     if plan._device != device:
         raise ValueError(f"the plan must be on {device}, got {plan._device}")
+    if not plan._fits:
+        raise ValueError("the plan's tensors are shorter than its numbers of sequences and parts")
     heads = shape[1]
     if kv_heads == 0 or heads % kv_heads:
         raise ValueError(f"q's heads must be a multiple of the cache's {kv_heads}, got {heads}")

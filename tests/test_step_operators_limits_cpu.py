@@ -46,3 +46,18 @@ def test_bindings_refuse_caches_without_heads_and_rows_without_channels():
     for group in (0, 32):
         with pytest.raises(ValueError, match="GPU" if group else "group must divide"):
             ssd.add_rms_norm_e4m3(zeros(3, 0), group=group)
+
+
+def test_plans_whose_tensors_are_too_short_are_refused():
+    """A plan with other numbers than its tensors were made for."""
+    sizes = dict(seq_lens=3, cu_seqlens=4, part_start=4, part_seq=20, part_keys=1, error_flag=1)
+
+    def call(**other):
+        plan = ssd.AttentionPlan(3, 3, 1, 0, 20, **{n: zeros(k, dtype=I32) for n, k in dict(sizes, **other).items()})
+        ssd.paged_attention_step(zeros(3, 4, 64), zeros(4, 2, 16, 64), zeros(4, 2, 64, 16), zeros(3, 4, dtype=I32), plan)
+
+    with pytest.raises(ValueError, match="on a GPU"):
+        call()
+    for name, size in sizes.items():
+        with pytest.raises(ValueError, match="shorter"):
+            call(**{name: size - 1})
