@@ -695,10 +695,10 @@ ssd_status ssd_attention_plan_build(const ssd_attention_plan *plan, void *stream
  * over the keys i <= p (and i > p - window, window > 0), and
  *     lse[t,h] = log sum_i e_i.
  * Tokens that see no key (an empty sequence, or p < 0), or only such whose
- * products are all -infinity, get 0 and lse -infinity; a NaN among the products
- * makes both NaN. What the cache holds where a token does not see it has no
- * effect, whatever it is. Rows of q behind
- * the last sequence's (a padded batch) leave theirs of out and lse as they were.
+ * products are all -infinity, get 0 and lse -infinity; a NaN or +infinity among
+ * the products makes both NaN. What the cache holds where a token does not see it
+ * has no effect, whatever it is. Rows of q behind the last sequence's (a padded
+ * batch) leave theirs of out and lse as they were.
  *  q, out          element type `dtype`, (total_tokens, nheads, head_dim), rows
  *                  *_stride elements apart (at least the row, at most 2^26)
  *  k_cache, v_cache  as in ssd_kv_cache_write, 16-byte aligned

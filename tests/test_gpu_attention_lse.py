@@ -38,3 +38,19 @@ def test_a_part_whose_keys_are_all_nan(D, dtype):
     out, lse = att.call(i)
     assert torch.isnan(out[:, 4:]).all() and torch.isnan(lse[:, 4:]).all()
     assert torch.equal(out[:, :4], clean[:, :4]) and torch.equal(lse[:, :4], clean_lse[:, :4])
+
+
+@pytest.mark.parametrize("lengths", [[150, 33], [4000, 700]])
+@pytest.mark.parametrize("D,dtype", [(128, BF), (64, F32)])
+def test_products_past_the_largest_number(lengths, D, dtype):
+    """One finite key whose product with every query of its head is +infinity: NaN for the tokens that see it."""
+    i = att.inputs(lengths, [2, 2], 8, 2, D, 16, dtype, seed=54)
+    i["q"].abs_()
+    clean, clean_lse = att.call(i)
+    at = lengths[0] - 1   # the second token's own
+    i["kc"][int(i["table"][0, at // 16]), 1, at % 16] = 3e38
+    out, lse = att.call(i)
+    hit = torch.zeros_like(lse, dtype=torch.bool)
+    hit[1, 4:] = True
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
