@@ -8,7 +8,7 @@
 // Memory-bound: x, the residual and the outputs pass once; a row stays in the
 // registers of its team of lanes (lane l holds vectors l, l + TEAM, ..) between
 // the loads, the sum of squares, the maxima and the stores. 35576 x 4096 bf16 to
-// e4m3 in groups of 128 takes 168 us, 6.1 TB/s (a large copy reaches 5.1).
+// e4m3 in groups of 128 takes 168 to 184 us, 5.6 to 6.1 TB/s (a large copy reaches 5.1).
 #include <algorithm>
 
 #include "ssd_norm.hpp"
@@ -26,8 +26,8 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
 
 // f / scale in float32 for V values, of which those past 512 only stay past it: the product with the reciprocal, whose two
 // roundings would move quotients half way between two codes off it, and one step by what it leaves of f. (Divisions would
-// be a third more instructions, this is a tenth: 35576 x 4096 bf16 takes as long as without, rows whose values are moved
-// one by one 5 % longer.)
+// be a third more instructions; this and the scales' own division are a seventh: 35576 x 4096 bf16 takes as long as
+// without, rows whose values are moved one by one 5 % longer.)
 template <int V> __device__ __forceinline__ void divide_all(float *f, float scale) {
     const float per = 1.0f / scale, by = fabsf(scale) == INFINITY ? 0.0f : scale;   // (0 x infinity is no 0)
 #pragma unroll

@@ -201,7 +201,11 @@ template <typename T, int D> struct AttnShape {
     static constexpr int STAGE = KROWS * KPITCH > DV * VPITCH ? KROWS * KPITCH : DV * VPITCH;
 };
 
-// STREAM: nobody else reads the keys and values that a workgroup does (one tile of rows).
+// STREAM: no other workgroup of the same sequence reads the keys and values that this one does (one tile of rows). Those of
+// other sequences may, where tables share the blocks of a prefix; the host does not see that, and the policy then costs
+// what it gains elsewhere, or more. With / without it, 32 heads of 128 on 8, bf16, us: 64 sequences of 4096 shared keys and
+// some 300 of their own 84 / 81 (no block shared 187 / 211), 256 of 2048 and 100 154 / 137 (355 / 397), 16 of 16384 and
+// 500 106 / 76 (180 / 204).
 template <typename T, int D, bool STREAM>
 __global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(D > 128 ? 1 : 2))) void ssd_attention_kernel(AttnArgs a) {
     using SH = AttnShape<T, D>;
@@ -594,7 +598,9 @@ __global__ __launch_bounds__(256) void ssd_kv_write_kernel(KvWriteArgs a) {
 // The same for many tokens: 64 tokens of one head a workgroup, the values turned in LDS, so that a store's lanes are
 // tokens, whose places in a prompt's block follow each other: a store writes whole lines of the values (single values
 // scattered took 6 times as long). 35576 tokens x 8 heads x 128 bf16 take 55 us, 5.3 TB/s, a large copy's rate; 69 without
-// the streaming policy on what is read and on the keys, 80 with it on the values too, whose lines two stores fill.
+// the streaming policy on what is read and on the keys, 80 with it on the values too, whose lines two stores fill. Other
+// rows, times a copy's: 1.1 (64 values bf16), 1.0 (64 and 256 float32), but 1.8 to 1.9 for 256 bf16 and 128 float32 (219 and
+// 207 us for 35576 x 8), whose two tiles, wholly in registers, leave one wave a SIMD.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void ssd_kv_write_tile_kernel(KvWriteArgs a) {
     constexpr int W = 16 / sizeof(T), PER = D / W, ROW = D * sizeof(T) + 8;   // 16-byte pieces of a row; its bytes in LDS
@@ -691,9 +697,10 @@ hipError_t launch_attention(const AttnArgs &a, bool bf16, int D, hipStream_t str
     return bf16 ? launch_attention_t<__bf16>(a, D, stream) : launch_attention_t<float>(a, D, stream);
 }
 
-// From this many rows of heads on the values are turned in LDS (a prompt of 512 / 1024 tokens x 8 heads 5.6 / 6.5 us, 6.2 /
-// 10.2 without; 2048 / 4096 x 2 heads 5.5 / 6.1, 4.5 / 6.6 without; 512 / 1024 single tokens x 8 heads 14.0 / 16.3, 7.9 /
-// 23.2 without).
+// From this many rows of heads on the values are turned in LDS (128 bf16: a prompt of 512 / 1024 tokens x 8 heads 5.6 / 6.5
+// us, 6.2 / 10.2 without; 2048 / 4096 x 2 heads 5.5 / 6.1, 4.5 / 6.6 without; 512 / 1024 single tokens x 8 heads 14.0 / 16.3,
+// 7.9 / 23.2 without. Prompts of 1024 x 8 of the other rows, 64 and 256 bf16, 64, 128 and 256 float32: 3.7, 10.7, 4.7, 9.9 and
+// 9.5; 6.7, 15.9, 7.7, 12.7 and 19.0 without).
 constexpr int64_t kTileRows = 8192;
 
 template <typename T> static hipError_t launch_kv_write_t(const KvWriteArgs &a, hipStream_t stream) {

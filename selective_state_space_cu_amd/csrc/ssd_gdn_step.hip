@@ -28,7 +28,8 @@ constexpr int kGdnStepThreads = 64;
 // One / two / four rows, 32 heads x 128 rows, us: dk 128 with 4 sequences 5.7 / 6.2 / 7.2, 8 9.0 / 8.0 / 8.6, 16 16.2 / 14.7 /
 // 13.2, 24 22.0 / 21.8, 32 27.0 / 27.9 / 29.0, 128 95 / 98 / 106; dk 64 with 4 4.8 / 5.1 / 6.4, 8 6.9 / 5.9, 16 11.0 / 8.5 /
 // 8.2, 128 55.8 / 52.4 / 55.3; dk 256 (16 heads x 256 rows) with 4 8.3 / 8.3 / 9.0, 64 90 / 93 / 95. A wave is a workgroup;
-// two or four take 0 to 2 % longer.
+// two or four take 0 to 2 % longer. (Four rows gain in a narrow band alone, 16 sequences here, 4 to 10 %, and lose on both
+// sides of it; they are not built.)
 static int gdn_step_rows(int dk, int64_t waves) { return dk <= 128 && waves > 2048 && (dk == 64 || waves < 16384) ? 2 : 1; }
 
 // Sum over the 8 lanes of a row; every lane gets it.
