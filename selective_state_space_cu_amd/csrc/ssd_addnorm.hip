@@ -27,7 +27,7 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
 // f / scale in float32 for V values, of which those past 512 only stay past it: the product with the reciprocal, whose two
 // roundings would move quotients half way between two codes off it, and one step by what it leaves of f. (Divisions would
 // be a third more instructions; this and the scales' own division are a seventh: 35576 x 4096 bf16 takes as long as
-// without, rows whose values are moved one by one 5 % longer.)
+// without, 35576 x 5120 2 % longer, one row 0.1 us.)
 template <int V> __device__ __forceinline__ void divide_all(float *f, float scale) {
     const float per = 1.0f / scale, by = fabsf(scale) == INFINITY ? 0.0f : scale;   // (0 x infinity is no 0)
 #pragma unroll
@@ -196,17 +196,23 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void ssd_add_rms_norm_kerne
             for (int r = 0; r < R; ++r)
                 if (live(r)) scale[r] = scale_of(top[(r * SPAN + lane * V) / a.group]);
         }
+        // RUN vectors divided at a time: all of a lane's where values are moved one by one, so that they take the reciprocal
+        // of their one scale once (20000 x 4097 bf16 172 us, 195 with 16 reciprocals); one where they are wide, two at a
+        // time need half as many registers again (35576 x 5120 bf16, a scale a row, 230 us for 220).
+        constexpr int RUN = V == 1 && (Q == kGiven || Q == kRowScale) ? R : 1;
         uint8_t *out = reinterpret_cast<uint8_t *>(a.out) + row * a.out_stride + lane * V;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (!live(r)) continue;
             float *f = v + r * V;
-            if (fabsf(scale[r]) < 0x1p-100f) {   // whose reciprocal may be infinite
-                scale[r] *= 0x1p100f;
+            if (r % RUN == 0) {
+                if (fabsf(scale[r]) < 0x1p-100f) {   // whose reciprocal may be infinite
+                    scale[r] *= 0x1p100f;
 #pragma unroll
-                for (int i = 0; i < V; ++i) f[i] *= 0x1p100f;
+                    for (int i = 0; i < RUN * V; ++i) f[i] *= 0x1p100f;
+                }
+                divide_all<RUN * V>(f, scale[r]);
             }
-            divide_all<V>(f, scale[r]);
             if constexpr (V == 8) {
                 *reinterpret_cast<u32x2 *>(out + r * SPAN) = u32x2{pack_e4m3(f[0], f[1], f[2], f[3]), pack_e4m3(f[4], f[5], f[6], f[7])};
             } else if constexpr (V == 4) {
